@@ -315,3 +315,13 @@ def ssd_scan(x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus_flag=True, h
     if rc != 0:
         raise ValueError("oracle_ssd_scan: bad arguments")
     return out, last
+
+
+from .recurrent import (  # noqa: E402,F401
+    beam_reorder,
+    beam_select,
+    causal_conv1d_bwd,
+    gated_scan,
+    gated_scan_bwd,
+    gated_state_update,
+)
