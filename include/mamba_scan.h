@@ -49,9 +49,9 @@
 extern "C" {
 #endif
 
-#define MSS_VERSION 20000 /* major * 10000 + minor * 100 + patch */
+#define MSS_VERSION 20100 /* major * 10000 + minor * 100 + patch */
 
-typedef enum { MSS_F32 = 0, MSS_BF16 = 1, MSS_I32 = 2 } mss_dtype_t;  /* I32: lengths only */
+typedef enum { MSS_F32 = 0, MSS_BF16 = 1, MSS_I32 = 2 } mss_dtype_t;  /* I32: lengths, beams, tokens */
 
 typedef enum {
     MSS_OK = 0,
@@ -379,6 +379,126 @@ int mss_ssd_scan_fwd(const mss_tensor_t* x, const mss_tensor_t* dt, const mss_te
                      const mss_tensor_t* B, const mss_tensor_t* C, const mss_tensor_t* D,
                      const mss_tensor_t* z, const mss_tensor_t* dt_bias, int softplus_flag,
                      const mss_tensor_t* out, const mss_tensor_t* last_state, void* stream);
+
+/*
+ * ---- Gated scan, the conv's gradients, beam search.
+ * These entry points own no device memory: scratch is the caller's, an f32 tensor (n,), 16-byte
+ * aligned, of at least the floats that the matching _scratch function names (it looks at sizes
+ * alone and makes no HIP call); NULL where that is 0.  What scratch holds before and after a call
+ * means nothing.  Calls that may run at the same time (other streams, host threads, captured graphs)
+ * need scratch of their own.  All of them can be captured with no call before, and give the same
+ * bits on every run.
+ *
+ * Gated scan: a linear recurrence with one state per channel and input-dependent decay.  For every
+ * batch b and channel d, with the raw gates fgate, igate:
+ *     r_t = sigmoid(fgate_t),  a_t = exp(-rate[d] r_t)
+ *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(igate_t) x_t,    out_t = h_t
+ * (the input's weight sqrt(1 - a^2) keeps the state's size as the decay changes).
+ *   x, fgate, igate  (batch, d_inner, L)   f32 or bf16, one dtype
+ *   rate             (d_inner,)            f32, positive (0 holds the state and lets nothing in; the
+ *                                          gradient to rate is taken as 0 through sqrt there; a negative
+ *                                          rate gives NaN)
+ *   initial_state    (batch, d_inner)      f32, nullable (zeros)
+ *   seq_lens         (batch,)              I32 in device memory, nullable (all L), clamped to [0, L] on
+ *                                          the device: past a sequence's end the state is held and out
+ *                                          is 0, whatever the inputs hold there
+ *   out              (batch, d_inner, L)   dtype of x, written; nullable
+ *   last_state       (batch, d_inner)      f32, written; nullable
+ *   saved_states     (batch, d_inner, ceil(L / 512)) f32, written with the state entering step 512 k,
+ *                                          for the backward; nullable
+ * At least one output (MSS_ERR_NULL_ARG).  No output may overlap an input or another output.
+ * Arithmetic and state are fp32; a row's inputs that are not finite make its later outputs not
+ * finite (infinite or NaN).  Rows that are whole aligned 16-byte vectors take aligned accesses,
+ * others element-aligned ones.
+ */
+int mss_gated_scan_scratch(int64_t batch, int64_t d_inner, int64_t L, int64_t* fwd_floats, int64_t* bwd_floats);
+int mss_gated_scan_fwd(const mss_tensor_t* x, const mss_tensor_t* fgate, const mss_tensor_t* igate,
+                       const mss_tensor_t* rate, const mss_tensor_t* initial_state,
+                       const mss_tensor_t* seq_lens, const mss_tensor_t* out,
+                       const mss_tensor_t* last_state, const mss_tensor_t* saved_states,
+                       const mss_tensor_t* scratch, void* stream);
+
+/*
+ * Gradients of the gated scan: dL/d(every input) given dout = dL/dout and dlast_state =
+ * dL/d last_state (nullable: 0), by the chain rule (G_t = dout_t + a_{t+1} G_{t+1}).
+ *   x, fgate, igate, rate, seq_lens   as passed to the forward
+ *   saved_states         as the forward wrote it for these inputs (it carries initial_state; a call
+ *                        with out and last_state NULL writes it alone)
+ *   dout                 (batch, d_inner, L)  dtype of x
+ *   dx, dfgate, digate   (batch, d_inner, L)  dtype of x, written (0 past a sequence's end)
+ *   drate                (d_inner,)           f32, written (sum over batch and time, fixed order)
+ *   dinitial_state       (batch, d_inner)     f32, nullable, written
+ */
+int mss_gated_scan_bwd(const mss_tensor_t* x, const mss_tensor_t* fgate, const mss_tensor_t* igate,
+                       const mss_tensor_t* rate, const mss_tensor_t* seq_lens,
+                       const mss_tensor_t* saved_states, const mss_tensor_t* dout,
+                       const mss_tensor_t* dlast_state, const mss_tensor_t* dx,
+                       const mss_tensor_t* dfgate, const mss_tensor_t* digate, const mss_tensor_t* drate,
+                       const mss_tensor_t* dinitial_state, const mss_tensor_t* scratch, void* stream);
+
+/*
+ * One token of the gated scan: state (batch, d_inner) f32, updated in place; x, fgate, igate
+ * (batch, d_inner) f32 or bf16; rate (d_inner,) f32; out (batch, d_inner) dtype of x, written with
+ * the new state.  state and out may not overlap an input or each other.
+ */
+int mss_gated_state_update(const mss_tensor_t* state, const mss_tensor_t* x, const mss_tensor_t* fgate,
+                           const mss_tensor_t* igate, const mss_tensor_t* rate, const mss_tensor_t* out,
+                           void* stream);
+
+/*
+ * Gradients of mss_causal_conv1d_fwd given dout = dL/dout and dfinal_state = dL/d final_state
+ * (nullable: 0).
+ *   x, weight, bias, initial_state, silu_flag   as passed to the forward
+ *   dout            (batch, d_inner, L)      dtype of x
+ *   dfinal_state    (batch, d_inner, K - 1)  dtype of x, nullable
+ *   dx              (batch, d_inner, L)      dtype of x, written
+ *   dweight         (d_inner, K)             f32, written (sum over batch and time, fixed order)
+ *   dbias           (d_inner,)               f32, nullable, written (also when bias is NULL)
+ *   dinitial_state  (batch, d_inner, K - 1)  dtype of x, nullable, written (also when initial_state is
+ *                                            NULL: the gradient at zeros)
+ * K is at most 4.  No output may overlap an input or another output.
+ */
+int mss_causal_conv1d_bwd_scratch(int64_t batch, int64_t d_inner, int64_t L, int64_t K, int64_t* floats);
+int mss_causal_conv1d_bwd(const mss_tensor_t* x, const mss_tensor_t* weight, const mss_tensor_t* bias,
+                          const mss_tensor_t* initial_state, int silu_flag, const mss_tensor_t* dout,
+                          const mss_tensor_t* dfinal_state, const mss_tensor_t* dx,
+                          const mss_tensor_t* dweight, const mss_tensor_t* dbias,
+                          const mss_tensor_t* dinitial_state, const mss_tensor_t* scratch, void* stream);
+
+/*
+ * Beam search, one step: the k best continuations of every request's beams.
+ * Beam i goes on with token v at scores[i] + logits[i][v] - log sum exp(logits[i]); a finished beam
+ * has one continuation, end_token, at scores[i] itself.  A continuation whose score is -inf or not a
+ * number does not exist: masked logits (-inf), NaN logits (taken as -inf), a beam that was never used
+ * (scores -inf), a row with a logit of +inf.  Higher scores come first; equal scores go by beam,
+ * within a beam by logit, then by token.  Scores are formed and compared in 64 bits.
+ *   logits         (batch, beams, vocab)  f32 or bf16
+ *   scores         (batch, beams)         f32
+ *   finished       (batch, beams)         I32, nullable (no beam is); nonzero: at its end
+ *   end_token      in [0, vocab), or -1 for none (then finished must be NULL)
+ *   next_scores    (batch, k)             f32, written, best first; where continuations run out: -inf,
+ *                                         parent 0, token 0, not finished
+ *   parents        (batch, k)             I32, written: the beam that goes on
+ *   tokens         (batch, k)             I32, written
+ *   next_finished  (batch, k)             I32, nullable, written: the parent was finished, or the token is
+ *                                         end_token
+ * beams and k are at most 64 (MSS_ERR_UNSUPPORTED).  next_scores may be scores, and next_finished
+ * finished (the same buffer and shape: updated in place); no other overlap.
+ */
+int mss_beam_select_scratch(int64_t batch, int64_t beams, int64_t vocab, int64_t k, int64_t* floats);
+int mss_beam_select(const mss_tensor_t* logits, const mss_tensor_t* scores, const mss_tensor_t* finished,
+                    int end_token, const mss_tensor_t* next_scores, const mss_tensor_t* parents,
+                    const mss_tensor_t* tokens, const mss_tensor_t* next_finished,
+                    const mss_tensor_t* scratch, void* stream);
+
+/*
+ * The beams' states in their new order, in place: for each of the `count` tensors, row b * beams + j
+ * becomes what row b * beams + parents[b][j] was.  A parent outside [0, beams) leaves its row as it is.
+ *   states   count pointers to tensors (batch * beams, ...) of f32, bf16 or I32 (scan states, conv
+ *            windows, lengths, ...), written; none may overlap another or parents
+ *   parents  (batch, beams)  I32, beams at most 64 (MSS_ERR_UNSUPPORTED)
+ */
+int mss_beam_reorder(const mss_tensor_t* const* states, int count, const mss_tensor_t* parents, void* stream);
 
 /*
  * Frees every workspace buffer the library holds, on every device (current ones and those

@@ -24,6 +24,9 @@ EXPORTS = ("mss_selective_scan_fwd", "mss_selective_scan_fwd_with_state",
            "mss_selective_state_update", "mss_causal_conv1d_fwd", "mss_causal_conv1d_update", "mss_profile_enable", "mss_profile_fwd",
            "mss_release_workspaces", "mss_set_plan_overrides", "mss_selective_scan_fwd_noalloc",
            "mss_ssd_scan_fwd",
+           "mss_gated_scan_scratch", "mss_gated_scan_fwd", "mss_gated_scan_bwd", "mss_gated_state_update",
+           "mss_causal_conv1d_bwd_scratch", "mss_causal_conv1d_bwd",
+           "mss_beam_select_scratch", "mss_beam_select", "mss_beam_reorder",
            "mss_status_string", "mss_version")
 
 
@@ -122,6 +125,25 @@ def load_library(path: str = LIB_PATH):
             lib.mss_ssd_scan_fwd.restype = ctypes.c_int
             lib.mss_ssd_scan_fwd.argtypes = [_TP, _TP, _TP, _TP, _TP, _TP, _TP, _TP, ctypes.c_int, _TP, _TP,
                                              ctypes.c_void_p]
+            i64, i64p = ctypes.c_int64, ctypes.POINTER(ctypes.c_int64)
+            lib.mss_gated_scan_scratch.restype = ctypes.c_int
+            lib.mss_gated_scan_scratch.argtypes = [i64, i64, i64, i64p, i64p]
+            lib.mss_gated_scan_fwd.restype = ctypes.c_int
+            lib.mss_gated_scan_fwd.argtypes = [_TP] * 10 + [ctypes.c_void_p]
+            lib.mss_gated_scan_bwd.restype = ctypes.c_int
+            lib.mss_gated_scan_bwd.argtypes = [_TP] * 14 + [ctypes.c_void_p]
+            lib.mss_gated_state_update.restype = ctypes.c_int
+            lib.mss_gated_state_update.argtypes = [_TP] * 6 + [ctypes.c_void_p]
+            lib.mss_causal_conv1d_bwd_scratch.restype = ctypes.c_int
+            lib.mss_causal_conv1d_bwd_scratch.argtypes = [i64, i64, i64, i64, i64p]
+            lib.mss_causal_conv1d_bwd.restype = ctypes.c_int
+            lib.mss_causal_conv1d_bwd.argtypes = [_TP] * 4 + [ctypes.c_int] + [_TP] * 7 + [ctypes.c_void_p]
+            lib.mss_beam_select_scratch.restype = ctypes.c_int
+            lib.mss_beam_select_scratch.argtypes = [i64, i64, i64, i64, i64p]
+            lib.mss_beam_select.restype = ctypes.c_int
+            lib.mss_beam_select.argtypes = [_TP] * 3 + [ctypes.c_int] + [_TP] * 5 + [ctypes.c_void_p]
+            lib.mss_beam_reorder.restype = ctypes.c_int
+            lib.mss_beam_reorder.argtypes = [ctypes.POINTER(_TP), ctypes.c_int, _TP, ctypes.c_void_p]
             lib.mss_release_workspaces.restype = ctypes.c_int
             lib.mss_release_workspaces.argtypes = []
             lib.mss_set_plan_overrides.restype = ctypes.c_int

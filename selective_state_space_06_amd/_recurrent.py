@@ -1,0 +1,405 @@
+"""Torch front end of the gated scan, the causal conv's gradients and beam search (argument
+marshalling only, like _binding.py).
+
+These entry points take their scratch from the caller.  The functions below take it from torch's
+allocator on the current stream, so every call, and every captured graph, has its own; the bound
+steps keep theirs.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from ._binding import MssError, Tensor, _bound_stream, _desc, _ref, _stream_of, load_library
+
+SAVED_SPACING = 512  # steps between two of gated_scan_fwd_save's states
+
+
+# ------------------------------------------------------------------- raw calls (descriptors or None)
+
+def gated_scan_scratch(batch, d_inner, L):
+    """(floats of scratch mss_gated_scan_fwd needs, floats mss_gated_scan_bwd needs)."""
+    f, b = ctypes.c_int64(), ctypes.c_int64()
+    _raise(load_library().mss_gated_scan_scratch(batch, d_inner, L, ctypes.byref(f), ctypes.byref(b)),
+           "mss_gated_scan_scratch")
+    return f.value, b.value
+
+
+def causal_conv1d_bwd_scratch(batch, d_inner, L, K):
+    """Floats of scratch mss_causal_conv1d_bwd needs."""
+    n = ctypes.c_int64()
+    _raise(load_library().mss_causal_conv1d_bwd_scratch(batch, d_inner, L, K, ctypes.byref(n)),
+           "mss_causal_conv1d_bwd_scratch")
+    return n.value
+
+
+def beam_select_scratch(batch, beams, vocab, k):
+    """Floats of scratch mss_beam_select needs."""
+    n = ctypes.c_int64()
+    _raise(load_library().mss_beam_select_scratch(batch, beams, vocab, k, ctypes.byref(n)), "mss_beam_select_scratch")
+    return n.value
+
+
+def gated_scan_fwd_raw(x, fgate, igate, rate, initial_state, seq_lens, out, last_state, saved_states, scratch,
+                       stream) -> int:
+    return load_library().mss_gated_scan_fwd(_ref(x), _ref(fgate), _ref(igate), _ref(rate), _ref(initial_state),
+                                             _ref(seq_lens), _ref(out), _ref(last_state), _ref(saved_states),
+                                             _ref(scratch), stream)
+
+
+def gated_scan_bwd_raw(x, fgate, igate, rate, seq_lens, saved_states, dout, dlast_state, dx, dfgate, digate, drate,
+                       dinitial_state, scratch, stream) -> int:
+    return load_library().mss_gated_scan_bwd(_ref(x), _ref(fgate), _ref(igate), _ref(rate), _ref(seq_lens),
+                                             _ref(saved_states), _ref(dout), _ref(dlast_state), _ref(dx),
+                                             _ref(dfgate), _ref(digate), _ref(drate), _ref(dinitial_state),
+                                             _ref(scratch), stream)
+
+
+def gated_state_update_raw(state, x, fgate, igate, rate, out, stream) -> int:
+    return load_library().mss_gated_state_update(_ref(state), _ref(x), _ref(fgate), _ref(igate), _ref(rate),
+                                                 _ref(out), stream)
+
+
+def conv1d_bwd_raw(x, weight, bias, initial_state, silu_flag, dout, dfinal_state, dx, dweight, dbias,
+                   dinitial_state, scratch, stream) -> int:
+    return load_library().mss_causal_conv1d_bwd(_ref(x), _ref(weight), _ref(bias), _ref(initial_state),
+                                                int(silu_flag), _ref(dout), _ref(dfinal_state), _ref(dx),
+                                                _ref(dweight), _ref(dbias), _ref(dinitial_state), _ref(scratch),
+                                                stream)
+
+
+def beam_select_raw(logits, scores, finished, end_token, next_scores, parents, tokens, next_finished, scratch,
+                    stream) -> int:
+    return load_library().mss_beam_select(_ref(logits), _ref(scores), _ref(finished), int(end_token),
+                                          _ref(next_scores), _ref(parents), _ref(tokens), _ref(next_finished),
+                                          _ref(scratch), stream)
+
+
+def beam_reorder_raw(states, parents, stream) -> int:
+    return load_library().mss_beam_reorder(_pointers(states), len(states), _ref(parents), stream)
+
+
+def _pointers(descs):
+    """An array of pointers to descriptors (the caller keeps them alive)."""
+    return (ctypes.POINTER(Tensor) * max(1, len(descs)))(*[ctypes.pointer(d) for d in descs])
+
+
+# ------------------------------------------------------------------------------- torch front end
+
+def _raise(status, where):
+    if status != 0:
+        raise MssError(status, where)
+
+
+def _same_device(x, tensors):
+    for t in tensors:
+        if t is not None and t.device != x.device:
+            raise ValueError(f"libmamba_scan takes tensors of one device, got {x.device} and {t.device}")
+
+
+def _launch(raw, where, x, *args):
+    """raw(*args, stream) on the current stream of x's device."""
+    import torch
+    stream = _stream_of(x.device)
+    if stream is not None:
+        st = raw(*args, stream)
+    else:
+        with torch.cuda.device(x.device):
+            st = raw(*args, torch.cuda.current_stream(x.device).cuda_stream)
+    _raise(st, where)
+
+
+def _scratch(floats, device):
+    import torch
+    return torch.empty(floats, dtype=torch.float32, device=device) if floats else None
+
+
+def _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, out, last_state, saved_states, where):
+    _same_device(x, (fgate, igate, rate, initial_state, seq_lens, out, last_state, saved_states))
+    floats = gated_scan_scratch(*x.shape)[0] if x.ndim == 3 else 0
+    _launch(gated_scan_fwd_raw, where, x, _desc(x), _desc(fgate), _desc(igate), _desc(rate), _desc(initial_state),
+            _desc(seq_lens), _desc(out), _desc(last_state), _desc(saved_states), _desc(_scratch(floats, x.device)))
+
+
+def _saved_like(x):
+    import torch
+    return torch.empty((x.shape[0], x.shape[1], -(-x.shape[2] // SAVED_SPACING)), dtype=torch.float32,
+                       device=x.device)
+
+
+def gated_scan_fwd(x, fgate, igate, rate, initial_state=None, seq_lens=None, return_last_state=True, out=None,
+                   last_state=None):
+    """Gated scan (mss_gated_scan_fwd) on the current stream of x's device: per channel
+    h_t = a h_{t-1} + sqrt(1 - a^2) sigmoid(igate_t) x_t with a = exp(-rate sigmoid(fgate_t)), out = h.
+
+    x, fgate, igate: (batch, d_inner, L) float32 or bfloat16 (the gates before their sigmoid); rate:
+    (d_inner,) float32, positive; initial_state: (batch, d_inner) float32 (None: zeros); seq_lens:
+    (batch,) int32 on the device (None: all L; outputs past a sequence's end are 0).  Returns out (dtype
+    of x), or (out, last_state) with last_state (batch, d_inner) float32."""
+    import torch
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if return_last_state and last_state is None:
+        last_state = torch.empty(x.shape[:2], dtype=torch.float32, device=x.device)
+    _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, out, last_state if return_last_state else None, None,
+               "mss_gated_scan_fwd")
+    return (out, last_state) if return_last_state else out
+
+
+def gated_scan_fwd_save(x, fgate, igate, rate, initial_state=None, seq_lens=None, out=None, last_state=None,
+                        saved_states=None):
+    """gated_scan_fwd that also writes the states its backward starts from: saved_states
+    (batch, d_inner, ceil(L / 512)) float32, the state entering every 512th step.  Returns
+    (out, last_state, saved_states)."""
+    import torch
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    if last_state is None:
+        last_state = torch.empty(x.shape[:2], dtype=torch.float32, device=x.device)
+    if saved_states is None:
+        saved_states = _saved_like(x)
+    _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, out, last_state, saved_states, "mss_gated_scan_fwd")
+    return out, last_state, saved_states
+
+
+def gated_scan_bwd(x, fgate, igate, rate, dout, initial_state=None, seq_lens=None, dlast_state=None,
+                   return_dinitial_state=False, saved_states=None):
+    """Gradients of gated_scan_fwd for L = sum(dout * out) + sum(dlast_state * last_state), on the
+    current stream.  Returns a dict: dx, dfgate, digate in x's dtype, drate (d_inner,) float32 and, with
+    return_dinitial_state, dinitial_state (batch, d_inner) float32.
+    saved_states: what gated_scan_fwd_save wrote for this forward (it carries the initial state); None:
+    they are computed again here, from initial_state."""
+    import torch
+    if saved_states is None:
+        saved_states = _saved_like(x)
+        _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, None, None, saved_states, "mss_gated_scan_fwd")
+    _same_device(x, (fgate, igate, rate, seq_lens, saved_states, dout, dlast_state))
+    g = {n: torch.empty_like(x, memory_format=torch.contiguous_format) for n in ("dx", "dfgate", "digate")}
+    g["drate"] = torch.empty_like(rate, memory_format=torch.contiguous_format)
+    if return_dinitial_state:
+        g["dinitial_state"] = torch.empty(x.shape[:2], dtype=torch.float32, device=x.device)
+    floats = gated_scan_scratch(*x.shape)[1] if x.ndim == 3 else 0
+    _launch(gated_scan_bwd_raw, "mss_gated_scan_bwd", x, _desc(x), _desc(fgate), _desc(igate), _desc(rate),
+            _desc(seq_lens), _desc(saved_states), _desc(dout), _desc(dlast_state), _desc(g["dx"]),
+            _desc(g["dfgate"]), _desc(g["digate"]), _desc(g["drate"]), _desc(g.get("dinitial_state")),
+            _desc(_scratch(floats, x.device)))
+    return g
+
+
+def gated_state_update(state, x, fgate, igate, rate, out=None):
+    """One token of the gated scan (mss_gated_state_update) on the current stream; `state`
+    (batch, d_inner) float32 is updated in place.  x, fgate, igate: (batch, d_inner) float32 or
+    bfloat16.  Returns out (batch, d_inner) in x's dtype."""
+    import torch
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _same_device(x, (state, fgate, igate, rate, out))
+    _launch(gated_state_update_raw, "mss_gated_state_update", x, _desc(state), _desc(x), _desc(fgate), _desc(igate),
+            _desc(rate), _desc(out))
+    return out
+
+
+def causal_conv1d_bwd(x, weight, dout, bias=None, initial_state=None, silu=True, dfinal_state=None,
+                      return_dinitial_state=False):
+    """Gradients of causal_conv1d_fwd for L = sum(dout * out) + sum(dfinal_state * final_state), on the
+    current stream.  Returns a dict: dx in x's dtype, dweight (d_inner, K), dbias (d_inner,) float32
+    (also when bias is None) and, with return_dinitial_state, dinitial_state (batch, d_inner, K - 1) in
+    x's dtype."""
+    import torch
+    _same_device(x, (weight, dout, bias, initial_state, dfinal_state))
+    g = dict(dx=torch.empty_like(x, memory_format=torch.contiguous_format),
+             dweight=torch.empty_like(weight, memory_format=torch.contiguous_format),
+             dbias=torch.empty(weight.shape[:1], dtype=torch.float32, device=x.device))
+    if return_dinitial_state:
+        g["dinitial_state"] = torch.empty((x.shape[0], x.shape[1], weight.shape[1] - 1), dtype=x.dtype,
+                                          device=x.device)
+    # shapes that the query refuses are refused by the call itself, with its own status
+    ok = x.ndim == 3 and weight.ndim == 2 and 1 <= weight.shape[1] <= 4
+    floats = causal_conv1d_bwd_scratch(*x.shape, weight.shape[1]) if ok else 0
+    _launch(conv1d_bwd_raw, "mss_causal_conv1d_bwd", x, _desc(x), _desc(weight), _desc(bias), _desc(initial_state),
+            1 if silu else 0, _desc(dout), _desc(dfinal_state), _desc(g["dx"]), _desc(g["dweight"]),
+            _desc(g["dbias"]), _desc(g.get("dinitial_state")), _desc(_scratch(floats, x.device)))
+    return g
+
+
+def beam_select(logits, scores, finished=None, end_token=None, k=None, next_scores=None, parents=None, tokens=None,
+                next_finished=None):
+    """The k best continuations (k: as many as there are beams) of every request's beams
+    (mss_beam_select), on the current stream: by score + log softmax(logits), a finished beam going on
+    with end_token alone at its own score.
+
+    logits: (batch, beams, vocab) float32 or bfloat16; scores: (batch, beams) float32; finished:
+    (batch, beams) int32, nonzero for a beam at its end (needs end_token).  Returns (next_scores
+    float32, parents int32, tokens int32), each (batch, k), best first, and with `finished` given also
+    next_finished int32.  next_scores=scores and next_finished=finished update those in place."""
+    import torch
+    dev_ = logits.device
+    _same_device(logits, (scores, finished, next_scores, parents, tokens, next_finished))
+    shape = (logits.shape[0], scores.shape[-1] if k is None else int(k))
+    if next_scores is None:
+        next_scores = torch.empty(shape, dtype=torch.float32, device=dev_)
+    if parents is None:
+        parents = torch.empty(shape, dtype=torch.int32, device=dev_)
+    if tokens is None:
+        tokens = torch.empty(shape, dtype=torch.int32, device=dev_)
+    if next_finished is None and finished is not None:
+        next_finished = torch.empty(shape, dtype=torch.int32, device=dev_)
+    ok = logits.ndim == 3 and 1 <= logits.shape[1] <= 64 and 1 <= shape[1] <= 64 and logits.shape[2] >= 1
+    floats = beam_select_scratch(*logits.shape, shape[1]) if ok else 0
+    _launch(beam_select_raw, "mss_beam_select", logits, _desc(logits), _desc(scores), _desc(finished),
+            -1 if end_token is None else int(end_token), _desc(next_scores), _desc(parents), _desc(tokens),
+            _desc(next_finished), _desc(_scratch(floats, dev_)))
+    got = (next_scores, parents, tokens)
+    return got if next_finished is None else got + (next_finished,)
+
+
+def beam_reorder(states, parents):
+    """Every state (batch * beams, ...) in place: row b * beams + j becomes the row of beam
+    parents[b, j] (mss_beam_reorder), on the current stream.  states: a sequence of float32, bfloat16 or
+    int32 tensors (all layers' scan states and conv windows in one call); parents: (batch, beams) int32;
+    a parent outside [0, beams) leaves its row as it is.  Returns states."""
+    _same_device(parents, states)
+    descs = [_desc(t) for t in states]
+    _launch(beam_reorder_raw, "mss_beam_reorder", parents, descs, _desc(parents))
+    return states
+
+
+# ---------------------------------------------------------------------------------------- autograd
+
+_fns = {}
+
+
+def _function(name, make):
+    if name not in _fns:
+        _fns[name] = make()
+    return _fns[name]
+
+
+class GatedScanFunction:
+    """torch.autograd wrapper of the gated scan: GatedScanFunction.apply(x, fgate, igate, rate,
+    initial_state, seq_lens) -> (out, last_state), differentiable in x, fgate, igate, rate and
+    initial_state (initial_state, seq_lens may be None).  The forward keeps one state in 512 for the
+    backward.  To capture a training step in a graph, capture gated_scan_fwd_save and gated_scan_bwd:
+    autograd ends the process when it captures a backward of leaves that an eager graph still holds."""
+
+    @staticmethod
+    def apply(x, fgate, igate, rate, initial_state=None, seq_lens=None):
+        return _function("gated", _make_gated).apply(x, fgate, igate, rate, initial_state, seq_lens)
+
+
+def _make_gated():
+    import torch
+
+    class _Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, fgate, igate, rate, initial_state, seq_lens):
+            out, last, saved = gated_scan_fwd_save(x, fgate, igate, rate, initial_state=initial_state,
+                                                   seq_lens=seq_lens)
+            ctx.save_for_backward(x, fgate, igate, rate, seq_lens, saved)
+            ctx.has_state = initial_state is not None
+            return out, last
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dout, dlast):
+            x, fgate, igate, rate, seq_lens, saved = ctx.saved_tensors
+            g = gated_scan_bwd(x, fgate, igate, rate, dout.contiguous(), seq_lens=seq_lens,
+                               dlast_state=dlast.contiguous(), return_dinitial_state=ctx.has_state,
+                               saved_states=saved)
+            return g["dx"], g["dfgate"], g["digate"], g["drate"], g.get("dinitial_state"), None
+
+    return _Gated
+
+
+class CausalConv1dFunction:
+    """torch.autograd wrapper of the causal conv: CausalConv1dFunction.apply(x, weight, bias,
+    initial_state, silu) -> (out, final_state), differentiable in x, weight, bias and initial_state
+    (bias, initial_state may be None).  Graph capture: as for GatedScanFunction."""
+
+    @staticmethod
+    def apply(x, weight, bias=None, initial_state=None, silu=True):
+        return _function("conv", _make_conv).apply(x, weight, bias, initial_state, silu)
+
+
+def _make_conv():
+    import torch
+
+    from ._binding import causal_conv1d_fwd
+
+    class _Conv(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, initial_state, silu):
+            out, final = causal_conv1d_fwd(x, weight, bias, initial_state=initial_state, silu=silu,
+                                           return_final_state=True)
+            ctx.save_for_backward(x, weight, bias, initial_state)
+            ctx.silu = silu
+            return out, final
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dout, dfinal):
+            x, weight, bias, initial_state = ctx.saved_tensors
+            g = causal_conv1d_bwd(x, weight, dout.contiguous(), bias=bias, initial_state=initial_state,
+                                  silu=ctx.silu, dfinal_state=dfinal.contiguous(),
+                                  return_dinitial_state=initial_state is not None)
+            return (g["dx"], g["dweight"], g["dbias"] if bias is not None else None, g.get("dinitial_state"), None)
+
+    return _Conv
+
+
+# ------------------------------------------------------------------------------------- bound steps
+
+def _empty_on(stream, shape, dtype, device):
+    """Memory whose earlier users are ordered before work on `stream` (a raw handle)."""
+    import torch
+    with torch.cuda.device(device):
+        if stream == torch.cuda.current_stream(device).cuda_stream:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+class GatedUpdateStep:
+    """mss_gated_state_update bound to fixed device buffers, for decode loops that refill the same
+    input buffers every token: descriptors and stream are taken once, here.  Arguments as for
+    gated_state_update; calling it updates `state` in place and writes `out` (returned)."""
+
+    def __init__(self, state, x, fgate, igate, rate, out=None, stream=None):
+        _same_device(x, (state, fgate, igate, rate, out))
+        stream = _bound_stream(x, stream)
+        self.out = _empty_on(stream, x.shape, x.dtype, x.device) if out is None else out
+        self._keep = (state, x, fgate, igate, rate, self.out)
+        self._descs = [_desc(t) for t in self._keep]
+        self._args = tuple(_ref(d) for d in self._descs) + (stream,)
+        self._fn = load_library().mss_gated_state_update
+
+    def __call__(self):
+        _raise(self._fn(*self._args), "mss_gated_state_update")
+        return self.out
+
+
+class BeamSearchStep:
+    """One step of a beam search bound to fixed device buffers: mss_beam_select on `logits` with
+    `scores` (and `finished`) updated in place, then mss_beam_reorder of `states` by the parents it
+    chose.  Arguments as for beam_select and beam_reorder; calling it returns (parents, tokens), its own
+    (batch, beams) int32 buffers, which the next call overwrites."""
+
+    def __init__(self, logits, scores, states, finished=None, end_token=None, stream=None):
+        import torch
+        _same_device(logits, (scores, finished, *states))
+        stream = _bound_stream(logits, stream)
+        self.parents = _empty_on(stream, scores.shape, torch.int32, logits.device)
+        self.tokens = _empty_on(stream, scores.shape, torch.int32, logits.device)
+        floats = beam_select_scratch(*logits.shape, scores.shape[-1])
+        scratch = _empty_on(stream, (floats,), torch.float32, logits.device)
+        self._keep = (logits, scores, finished, self.parents, self.tokens, scratch, *states)
+        lo, sc, fi, pa, to, scr, *sts = [_desc(t) for t in self._keep]
+        self._descs = (lo, sc, fi, pa, to, scr, sts)
+        self._select_args = (_ref(lo), _ref(sc), _ref(fi), -1 if end_token is None else int(end_token), _ref(sc),
+                             _ref(pa), _ref(to), _ref(fi), _ref(scr), stream)
+        self._reorder_args = (_pointers(sts), len(sts), _ref(pa), stream)
+        self._lib = load_library()
+
+    def __call__(self):
+        _raise(self._lib.mss_beam_select(*self._select_args), "mss_beam_select")
+        _raise(self._lib.mss_beam_reorder(*self._reorder_args), "mss_beam_reorder")
+        return self.parents, self.tokens

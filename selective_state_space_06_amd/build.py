@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmamba_scan.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["abi.hip", "scan_fwd.hip", "scan_fast.hip", "scan_bwd.hip", "state_update.hip", "conv1d.hip",
-           "ssd_scan.hip"]
+           "ssd_scan.hip", "gated_scan.hip", "conv1d_bwd.hip", "beam.hip", "abi_recurrent.hip"]
 ARCH = "gfx950"
 
 

@@ -169,4 +169,95 @@ int plan_bwd_segments(const BwdLaunch& a, int num_cus, int segments_override);
 size_t bwd_workspace_bytes(const BwdLaunch& a, int segments);
 hipError_t launch_scan_bwd(const BwdLaunch& a, int segments, void* workspace, hipStream_t stream);
 
+// Gated scan (gated_scan.hip): x, f, i, out and their gradients (Bt, Dn, L); rate (Dn); states (Bt, Dn).
+constexpr int kGatedTile = 512;  // steps between two saved states
+
+struct GatedLaunch {
+    const void* x = nullptr;
+    const void* f = nullptr;
+    const void* i = nullptr;
+    const float* rate = nullptr;
+    const float* h0 = nullptr;       // nullable
+    const int32_t* lens = nullptr;   // nullable
+    void* out = nullptr;             // nullable when saved is given
+    float* last_state = nullptr;     // nullable
+    float* saved = nullptr;          // (Bt, Dn, ceil(L / 512)); the forward's is nullable
+    // the backward's
+    const void* dout = nullptr;
+    const float* dlast = nullptr;    // nullable
+    void* dx = nullptr;
+    void* df = nullptr;
+    void* di = nullptr;
+    float* drate = nullptr;
+    float* dh0 = nullptr;            // nullable
+    float* scratch = nullptr;
+    int64_t Bt = 0, Dn = 0, L = 0;
+    bool bf16 = false;
+    bool vec_ok = false;             // rows of every (Bt, Dn, L) tensor are whole aligned 16-byte vectors
+};
+
+struct GatedUpdateLaunch {
+    float* state;                    // (Bt, Dn), in/out
+    const void* x;
+    const void* f;
+    const void* i;
+    const float* rate;
+    void* out;
+    int64_t Dn, R;                   // R = Bt * Dn
+    bool bf16;
+};
+// Scratch floats of the forward and the backward, by sizes alone.
+int64_t gated_fwd_scratch(int64_t Bt, int64_t Dn, int64_t L);
+int64_t gated_bwd_scratch(int64_t Bt, int64_t Dn, int64_t L);
+hipError_t launch_gated_fwd(const GatedLaunch& a, hipStream_t stream);
+hipError_t launch_gated_bwd(const GatedLaunch& a, hipStream_t stream);
+hipError_t launch_gated_update(const GatedUpdateLaunch& a, hipStream_t stream);
+
+// Causal conv1d's gradients (conv1d_bwd.hip).
+struct ConvBwdLaunch {
+    const void* x;
+    const float* w;
+    const float* bias;      // nullable
+    const void* state_in;   // (Bt, Dn, K-1), nullable
+    const void* dout;
+    const void* dfinal;     // (Bt, Dn, K-1), nullable
+    void* dx;
+    float* dw;              // (Dn, K)
+    float* db;              // nullable
+    void* dstate;           // (Bt, Dn, K-1), nullable
+    float* scratch;
+    int64_t Dn, L, R;       // R = Bt * Dn
+    int K;
+    bool silu, bf16;
+    bool vec_ok;            // rows of x / dout / dx are whole aligned 16-byte vectors
+};
+int64_t conv1d_bwd_scratch(int64_t Bt, int64_t Dn, int64_t L, int64_t K);
+hipError_t launch_conv1d_bwd(const ConvBwdLaunch& a, hipStream_t stream);
+
+// Beam search (beam.hip).
+constexpr int kBeamMost = 64;     // beams, and continuations kept, per request
+constexpr int kReorderMost = 32;  // state tensors per launch
+
+struct BeamSelectLaunch {
+    const void* logits;           // (Bt, N, V)
+    const float* scores;          // (Bt, N)
+    const int32_t* finished;      // (Bt, N), nullable
+    float* next_scores;           // (Bt, K)
+    int32_t* parents;
+    int32_t* tokens;
+    int32_t* next_finished;       // nullable
+    float* scratch;
+    int64_t Bt, N, V, K;
+    int end;                      // -1: no end token
+    bool bf16, vec_ok;            // rows of logits are whole aligned 16-byte vectors
+};
+struct BeamReorderLaunch {
+    void* data;
+    int64_t bytes;                // of one beam's state
+};
+int64_t beam_select_scratch(int64_t Bt, int64_t N, int64_t V, int64_t K);
+hipError_t launch_beam_select(const BeamSelectLaunch& a, hipStream_t stream);
+hipError_t launch_beam_reorder(const BeamReorderLaunch* states, int count, const int32_t* parents, int64_t Bt, int N,
+                               hipStream_t stream);
+
 }  // namespace mss

@@ -1,0 +1,267 @@
+"""The gated scan, the conv's gradients and beam search without a GPU: every invalid call is refused
+with its documented status before any HIP call (the device addresses below are made up), calls with
+nothing to do return, and the scratch queries look at sizes alone."""
+import ctypes
+import os
+
+import pytest
+
+import selective_state_space_06_amd as mss
+from selective_state_space_06_amd import MSS_BF16, MSS_F32, MSS_I32, Tensor
+
+OK, NULL_ARG, SHAPE, DTYPE, LAYOUT, ALIAS, UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
+_next = [0x10000000]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not os.path.exists(mss.LIB_PATH):
+        from selective_state_space_06_amd import build
+        build.build()
+    return mss.load_library()
+
+
+def T(shape, dtype=MSS_F32):
+    n = 4
+    for s in shape:
+        n *= max(1, s)
+    a = _next[0]
+    _next[0] += (n + 0xFFFF) & ~0xFFFF
+    return Tensor.make(a, dtype, shape)
+
+
+def moved(t, nbytes):
+    return Tensor.make(t.data + nbytes, t.dtype, list(t.shape)[:t.ndim])
+
+
+def strided(t):
+    s = list(t.shape)[:t.ndim]
+    st, acc = [], 2
+    for e in reversed(s):
+        st.insert(0, acc)
+        acc *= e
+    return Tensor.make(t.data, t.dtype, s, st)
+
+
+B, D, L, K, NV = 2, 64, 700, 4, 1000
+
+
+def scan_args(dt=MSS_BF16):
+    return dict(x=T([B, D, L], dt), fgate=T([B, D, L], dt), igate=T([B, D, L], dt), rate=T([D]),
+                initial_state=T([B, D]), seq_lens=T([B], MSS_I32), out=T([B, D, L], dt), last_state=T([B, D]),
+                saved_states=T([B, D, 2]), scratch=T([4096]))
+
+
+def bwd_args(dt=MSS_BF16):
+    return dict(x=T([B, D, L], dt), fgate=T([B, D, L], dt), igate=T([B, D, L], dt), rate=T([D]),
+                seq_lens=T([B], MSS_I32), saved_states=T([B, D, 2]), dout=T([B, D, L], dt), dlast_state=T([B, D]),
+                dx=T([B, D, L], dt), dfgate=T([B, D, L], dt), digate=T([B, D, L], dt), drate=T([D]),
+                dinitial_state=T([B, D]), scratch=T([4096]))
+
+
+def step_args(dt=MSS_BF16):
+    return dict(state=T([B, D]), x=T([B, D], dt), fgate=T([B, D], dt), igate=T([B, D], dt), rate=T([D]),
+                out=T([B, D], dt))
+
+
+def conv_args(dt=MSS_BF16):
+    return dict(x=T([B, D, L], dt), weight=T([D, K]), bias=T([D]), initial_state=T([B, D, K - 1], dt), silu_flag=1,
+                dout=T([B, D, L], dt), dfinal_state=T([B, D, K - 1], dt), dx=T([B, D, L], dt), dweight=T([D, K]),
+                dbias=T([D]), dinitial_state=T([B, D, K - 1], dt), scratch=T([1 << 16]))
+
+
+def select_args(dt=MSS_BF16, N=3, k=3):
+    return dict(logits=T([B, N, NV], dt), scores=T([B, N]), finished=T([B, N], MSS_I32), end_token=5,
+                next_scores=T([B, k]), parents=T([B, k], MSS_I32), tokens=T([B, k], MSS_I32),
+                next_finished=T([B, k], MSS_I32), scratch=T([1 << 16]))
+
+
+CALLS = {"scan": (scan_args, mss.gated_scan_fwd_raw), "bwd": (bwd_args, mss.gated_scan_bwd_raw),
+         "step": (step_args, mss.gated_state_update_raw), "conv": (conv_args, mss.conv1d_bwd_raw),
+         "select": (select_args, mss.beam_select_raw)}
+REQUIRED = {"scan": "x fgate igate rate", "step": "state x fgate igate rate out",
+            "bwd": "x fgate igate rate saved_states dout dx dfgate digate drate scratch",
+            "conv": "x weight dout dx dweight scratch",
+            "select": "logits scores next_scores parents tokens scratch"}
+OUTPUTS = {"scan": "out last_state saved_states", "bwd": "dx dfgate digate drate dinitial_state scratch",
+           "step": "state out", "conv": "dx dweight dbias dinitial_state scratch",
+           "select": "next_scores parents tokens next_finished scratch"}
+
+
+def call(op, a):
+    return CALLS[op][1](*a.values(), None)
+
+
+def each(names):
+    return [(op, n) for op, ns in names.items() for n in ns.split()]
+
+
+@pytest.mark.parametrize("op,name", each(REQUIRED))
+def test_null_required(op, name):
+    a = CALLS[op][0]()
+    a[name] = None
+    assert call(op, a) == NULL_ARG
+    a = CALLS[op][0]()
+    a[name].data = None
+    assert call(op, a) == NULL_ARG
+
+
+def test_scan_needs_an_output():
+    a = scan_args()
+    a.update(out=None, last_state=None, saved_states=None)
+    assert call("scan", a) == NULL_ARG
+
+
+@pytest.mark.parametrize("op", CALLS)
+def test_shape_dtype_layout_of_every_tensor(op):
+    for name, t in CALLS[op][0]().items():
+        if not isinstance(t, Tensor):
+            continue
+        shape = list(t.shape)[:t.ndim]
+        for j in range(t.ndim):
+            # the vocabulary stands in no other shape; these sizes need no scratch in the forward
+            if (op, name, j) in (("select", "logits", 2), ("scan", "scratch", 0)):
+                continue
+            a = CALLS[op][0]()
+            bad = list(shape)
+            bad[j] = 1 if name == "scratch" else bad[j] + 1
+            a[name] = Tensor.make(t.data, t.dtype, bad)
+            assert call(op, a) == SHAPE, (op, name, j)
+        a = CALLS[op][0]()
+        a[name] = Tensor.make(t.data, t.dtype, shape + [1])
+        assert call(op, a) == SHAPE, (op, name, "ndim")
+        a = CALLS[op][0]()
+        a[name] = Tensor.make(t.data, t.dtype, [-1] + shape[1:])
+        assert call(op, a) == SHAPE, (op, name, "negative")
+        for dt in (MSS_F32, MSS_BF16, MSS_I32, 7):
+            a = CALLS[op][0]()
+            if dt == a[name].dtype:
+                continue
+            if (op, name, dt) == ("select", "logits", MSS_F32):  # its own type stands alone
+                continue
+            a[name].dtype = dt
+            assert call(op, a) == DTYPE, (op, name, dt)
+        a = CALLS[op][0]()
+        a[name] = strided(a[name])
+        assert call(op, a) == LAYOUT, (op, name)
+        a = CALLS[op][0]()
+        a[name] = moved(a[name], 1)
+        assert call(op, a) == LAYOUT, (op, name)
+
+
+@pytest.mark.parametrize("op,name", each(OUTPUTS))
+def test_overlaps_are_refused(op, name):
+    for other, t in CALLS[op][0]().items():
+        if other == name or not isinstance(t, Tensor):
+            continue
+        a = CALLS[op][0]()
+        if (op, name, other) in (("select", "next_scores", "scores"), ("select", "next_finished", "finished")):
+            continue  # in place: allowed, and tested where it runs
+        esz = 2 if a[name].dtype == MSS_BF16 else 4
+        at = a[other].data
+        if at % 16 == 0 and a[name].data:
+            a[name].data = at
+        assert esz and call(op, a) == ALIAS, (op, name, other)
+
+
+def test_select_partial_overlap_with_scores_is_refused():
+    a = select_args()
+    a["next_scores"].data = a["scores"].data + 4
+    assert call("select", a) == ALIAS
+    a = select_args(k=2)  # the same address but another shape
+    a["next_scores"].data = a["scores"].data
+    assert call("select", a) == ALIAS
+
+
+def test_select_end_token_and_limits():
+    for end in (-2, NV, -1):  # -1 with finished given
+        a = select_args()
+        a["end_token"] = end
+        assert call("select", a) == SHAPE
+    assert call("select", select_args(N=65, k=3)) == UNSUPPORTED
+    assert call("select", select_args(N=3, k=65)) == UNSUPPORTED
+    a = select_args(k=0)
+    assert call("select", a) == SHAPE
+
+
+def test_conv_wide_kernel_is_unsupported():
+    a = conv_args()
+    a.update(weight=T([D, 5]), dweight=T([D, 5]), initial_state=None, dfinal_state=None, dinitial_state=None)
+    assert call("conv", a) == UNSUPPORTED
+
+
+def test_scratch_queries():
+    assert mss.gated_scan_scratch(4, 5120, 2048)[1] >= 4 * 5120
+    assert mss.causal_conv1d_bwd_scratch(4, 5120, 2048, 4) >= 5 * 4 * 5120
+    assert mss.beam_select_scratch(1, 1, 1, 1) >= 5
+    for f, args in ((mss.gated_scan_scratch, (-1, 4, 4)), (mss.gated_scan_scratch, (1 << 40, 1 << 40, 4)),
+                    (mss.causal_conv1d_bwd_scratch, (2, 4, 4, 0)), (mss.beam_select_scratch, (1, 0, 5, 1))):
+        with pytest.raises(mss.MssError) as e:
+            f(*args)
+        assert e.value.status == SHAPE
+    for f, args in ((mss.causal_conv1d_bwd_scratch, (2, 4, 4, 5)), (mss.beam_select_scratch, (1, 65, 5, 1))):
+        with pytest.raises(mss.MssError) as e:
+            f(*args)
+        assert e.value.status == UNSUPPORTED
+    n = ctypes.c_int64()
+    lib = mss.load_library()
+    assert lib.mss_gated_scan_scratch(1, 1, 1, None, ctypes.byref(n)) == NULL_ARG
+    assert lib.mss_causal_conv1d_bwd_scratch(1, 1, 1, 1, None) == NULL_ARG
+    assert lib.mss_beam_select_scratch(1, 1, 1, 1, None) == NULL_ARG
+
+
+@pytest.mark.parametrize("op", CALLS)
+def test_empty_batch_is_ok(op):
+    a = CALLS[op][0]()
+    for n, t in a.items():
+        if not isinstance(t, Tensor) or n in ("scratch", "rate", "drate", "weight", "bias", "dweight", "dbias"):
+            continue
+        shape = list(t.shape)[:t.ndim]
+        a[n] = Tensor.make(0, t.dtype, [0] + shape[1:])
+    if op in ("bwd", "conv"):  # the sums over an empty batch are still written: no channels either
+        for n, t in a.items():
+            if isinstance(t, Tensor) and n not in ("scratch", "seq_lens"):
+                shape = list(t.shape)[:t.ndim]
+                shape[1 if t.ndim >= 2 and n not in ("weight", "dweight") else 0] = 0
+                a[n] = Tensor.make(0, t.dtype, shape)
+    assert call(op, a) == OK
+
+
+def test_reorder_refusals():
+    par = T([B, 4], MSS_I32)
+    ok = [T([B * 4, 8, 16]), T([B * 4, 8, 3], MSS_BF16), T([B * 4], MSS_I32)]
+    raw = mss.beam_reorder_raw
+    assert raw([], par, None) == OK
+    assert raw([T([0, 5])], T([0, 4], MSS_I32), None) == OK
+    assert raw(ok, None, None) == NULL_ARG
+    nul = T([B * 4, 8])
+    nul.data = None
+    assert raw(ok + [nul], par, None) == NULL_ARG
+    assert raw(ok + [T([B * 4 + 1, 8])], par, None) == SHAPE
+    assert raw(ok, T([B, 4, 1], MSS_I32), None) == SHAPE
+    assert raw(ok, T([B, 4]), None) == DTYPE
+    assert raw(ok + [T([B * 4, 8], 7)], par, None) == DTYPE
+    assert raw(ok + [strided(T([B * 4, 8]))], par, None) == LAYOUT
+    assert raw(ok + [moved(T([B * 4, 8]), 2)], par, None) == LAYOUT
+    assert raw(ok + [moved(ok[0], 16)], par, None) == ALIAS
+    big = T([B * 4, 8])
+    assert raw([big], Tensor.make(big.data + 32, MSS_I32, [B, 4]), None) == ALIAS
+    assert raw([T([B * 65, 4])], T([B, 65], MSS_I32), None) == UNSUPPORTED
+    lib = mss.load_library()
+    assert lib.mss_beam_reorder(None, 1, ctypes.byref(par), None) == NULL_ARG
+    assert lib.mss_beam_reorder(None, -1, ctypes.byref(par), None) == SHAPE
+
+
+def test_front_end_refuses_host_tensors():
+    import torch
+    t = torch.zeros(2, 4, 8)
+    with pytest.raises(ValueError):
+        mss.gated_scan_fwd(t, t, t, torch.zeros(4))
+    with pytest.raises(ValueError):
+        mss.causal_conv1d_bwd(t, torch.zeros(4, 4), t)
+    with pytest.raises(ValueError):
+        mss.beam_select(t, torch.zeros(2, 4))
+    with pytest.raises(ValueError):
+        mss.beam_reorder([t], torch.zeros(1, 2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        mss.GatedUpdateStep(t[0], t[0], t[0], t[0], torch.zeros(8))
