@@ -58,9 +58,31 @@ def build_example(verbose: bool = False) -> str:
     return EXAMPLE_BIN
 
 
+NATIVE_SRC = os.path.join(CSRC, "native_calls.c")
+NATIVE_LIB = os.path.join(PKG_DIR, "_native.so")
+
+
+def build_native(verbose: bool = False) -> str:
+    """Compile the CPython module `_native` (host code only) against the built library, which it finds
+    beside itself. Returns its path."""
+    import sysconfig
+    tmp = NATIVE_LIB + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-std=c11", "-O2", "-Wall", "-Wextra", "-fPIC", "-shared", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], NATIVE_SRC, "-L", PKG_DIR, "-lmamba_scan", "-Wl,-rpath,$ORIGIN",
+           "-o", tmp]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        sys.stderr.write(proc.stdout + proc.stderr)
+        raise RuntimeError(f"compiling native_calls.c failed with exit code {proc.returncode}")
+    os.replace(tmp, NATIVE_LIB)
+    return NATIVE_LIB
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every source (in parallel, one object each) and link them into LIB_PATH
-    (atomically replaced), then the C example against it. Returns the library's path."""
+    (atomically replaced), then the `_native` module and the C example against it. Returns the library's path."""
     from concurrent.futures import ThreadPoolExecutor
 
     objdir = os.path.join(PKG_DIR, "_build")
@@ -89,6 +111,7 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         sys.stderr.write(proc.stdout + proc.stderr)
         raise RuntimeError(f"linking failed with exit code {proc.returncode}")
     os.replace(tmp, LIB_PATH)
+    build_native(verbose)
     build_example(verbose)
     return LIB_PATH
 

@@ -2,6 +2,7 @@
 // search: argument validation and dispatch.  Every check runs before the first HIP call.  These
 // entry points own no workspace: scratch comes from the caller, so calls on any streams, host
 // threads and captured graphs are independent as long as their scratch is.
+#include <algorithm>
 #include <vector>
 
 #include "abi_checks.hpp"
@@ -325,11 +326,15 @@ int mss_beam_reorder(const mss_tensor_t* const* states, int count, const mss_ten
         if (!laid_out({parents})) return MSS_ERR_LAYOUT;
         for (int t = 0; t < count; ++t)
             if (!laid_out({states[t]})) return MSS_ERR_LAYOUT;
-        for (int t = 0; t < count; ++t) {
-            if (overlap(states[t], parents)) return MSS_ERR_ALIAS;
-            for (int u = t + 1; u < count; ++u)
-                if (overlap(states[t], states[u])) return MSS_ERR_ALIAS;
+        std::vector<Range> used;
+        used.reserve(static_cast<size_t>(count) + 1);
+        for (int t = -1; t < count; ++t) {
+            const Range r = range_of(t < 0 ? parents : states[t]);
+            if (r.lo != r.hi) used.push_back(r);
         }
+        std::sort(used.begin(), used.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+        for (size_t t = 1; t < used.size(); ++t)
+            if (used[t].lo < used[t - 1].hi) return MSS_ERR_ALIAS;
         if (N > mss::kBeamMost) return MSS_ERR_UNSUPPORTED;
         if (Bt * N == 0 || count == 0) return MSS_OK;
         std::vector<mss::BeamReorderLaunch> l(static_cast<size_t>(count));

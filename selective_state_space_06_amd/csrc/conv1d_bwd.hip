@@ -8,17 +8,17 @@
 //     dw_k = sum over batch and time of dy_t window[t + k],   dbias = sum of dy_t
 // dx is dwindow past its first K - 1 entries, dinitial_state those.
 //
-// A wave walks a row from its end, 512 steps a round, eight to a lane: y needs the last K - 1 inputs
-// of the lane before (a whole-wave shift), dx the first K - 1 dy of the lane after; the first lane's
-// dy is kept for the round that precedes it in time.  The sums over time stay in registers.
+// A wave walks a row (or a segment of one) from its end, a tile of 512 steps a round, eight to a lane:
+// y needs the last K - 1 inputs of the lane before (a whole-wave shift; those before the tile
+// are loaded with it), dx the first K - 1 dy of the lane after; the first lane's dy is kept for the tile that
+// precedes it in time.  A tile's loads are issued before the one after it in time is computed.  The
+// sums over time stay in registers.
 #include "device_math.hpp"
 #include "mss_internal.hpp"
+#include "row_io.hpp"
 
 namespace mss {
 namespace {
-
-constexpr int kE = 8;
-constexpr int kTile = 64 * kE;
 
 struct CArgs {
     const void* x;
@@ -29,99 +29,89 @@ struct CArgs {
     const void* dfin;       // (R, K-1), nullable
     void* dx;
     void* dst;              // (R, K-1), nullable
-    float* part;            // (K + 1, R): the row's dw_0 .. dw_{K-1}, dbias
-    int64_t Dn, L, R;
+    float* dw;              // (Dn, K)
+    float* db;              // (Dn), nullable
+    float* part;            // (K + 1, R, S): a segment's dw_0 .. dw_{K-1}, dbias, when S > 1
+    int64_t Bt, Dn, L, R, tiles;
+    int64_t seg_tiles;      // tiles per segment
+    int S;                  // segments per row
 };
 
-template <class E, bool VEC>
-__device__ __forceinline__ void load8(const void* base, int64_t row, int64_t t0, int64_t L, float* v) {
-    constexpr int V = E::kPerVec;
-    const auto* p = static_cast<const typename E::storage*>(base) + row * L;
-#pragma unroll
-    for (int j = 0; j < kE / V; ++j) {
-        const int64_t t = t0 + j * V;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (t + V <= L) {
-            if (VEC) w = *reinterpret_cast<const uint4*>(p + t);
-            else __builtin_memcpy(&w, p + t, 16);
-            E::unpack(w, v + j * V);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[j * V + e] = (!VEC && t + e < L) ? E::load1(p, t + e) : 0.0f;
-        }
-    }
-}
-template <class E, bool VEC>
-__device__ __forceinline__ void store8(void* base, int64_t row, int64_t t0, int64_t L, const float* v) {
-    constexpr int V = E::kPerVec;
-    auto* p = static_cast<typename E::storage*>(base) + row * L;
-#pragma unroll
-    for (int j = 0; j < kE / V; ++j) {
-        const int64_t t = t0 + j * V;
-        const uint4 w = E::pack(v + j * V);
-        if (t + V <= L) {
-            if (VEC) *reinterpret_cast<uint4*>(p + t) = w;
-            else __builtin_memcpy(p + t, &w, 16);
-        } else if (!VEC) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (t + e < L) E::store1(p, t + e, v[j * V + e]);
-        }
-    }
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float old, float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, 0xF, 0xF, false));
-}
-__device__ __forceinline__ float lane_of(float v, int lane) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+// dy = dout silu'(y)
+__device__ __forceinline__ float silu_grad(float y) {
+    const float s = fast_rcp(1.0f + fast_exp2(-y * kLog2e));
+    return s * fmaf(y, 1.0f - s, 1.0f);
 }
 
+// Five waves a SIMD for aligned bf16 rows (2.8B layer: 52.6 us, 54.5 at four); the others would spill (8 x
+// 1536 x 2047 f32: 58 us at four, 70 at five).
 template <class E, int K, bool SILU, bool VEC>
-__global__ __launch_bounds__(256) void conv_bwd_kernel(CArgs a) {
+__global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_kernel(CArgs a) {
+    using S = typename E::storage;
+    __shared__ float sums[4][K + 1];
     const int lane = threadIdx.x & 63;
-    const int64_t tiles = (a.L + kTile - 1) / kTile;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.R; row += (int64_t)gridDim.x * 4) {
-        const int64_t ch = row % a.Dn;
-        float w[K], dw[K], db = 0.0f, later[K];  // later: the first K - 1 dy of the following round
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    const int64_t items = a.R * a.S;
+    // One row's segment; adds the wave's dw_0 .. dw_{K-1}, dbias to s.
+    const auto pass = [&](int64_t row, int seg, float* s) {
+        const int64_t first = seg * a.seg_tiles;
+        const int64_t end = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
+        const int64_t ch = row % a.Dn, base = row * a.L;
+        const S* xr = static_cast<const S*>(a.x) + base;
+        float w[K], dw[K], db = 0.0f, later[K];  // later: the first K - 1 dy of the following tile
 #pragma unroll
         for (int k = 0; k < K; ++k) w[k] = a.w[ch * K + k], dw[k] = 0.0f, later[k] = 0.0f;
         const float b = a.bias ? a.bias[ch] : 0.0f;
-        const auto* xr = static_cast<const typename E::storage*>(a.x) + row * a.L;
-        for (int64_t t = tiles - 1; t >= 0; --t) {
-            const int64_t t0 = t * kTile + lane * kE;
-            float v[K - 1 + kE], d[kE + K - 1], o[kE];
-            load8<E, VEC>(a.x, row, t0, a.L, v + K - 1);
-            load8<E, VEC>(a.dout, row, t0, a.L, d);
-            // the K - 1 inputs before this lane's: from the lane below, for the first lane from the
-            // row (always inside it: t0 is at least 512 then) or the carried state
+        if (K > 1 && end < a.tiles) {  // the following segment's first dy, a lane each
+            const int64_t t = end * kTile + lane;
+            float dy = 0.0f;
+            if (lane < K - 1 && t < a.L) {
+                dy = E::load1(a.dout, base + t);
+                if (SILU) {
+                    float y = b;
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) {
-                float first = 0.0f;
-                if (lane == 0) {
-                    if (t > 0) first = E::load1(xr, t0 - (K - 1) + j);
-                    else if (a.st) first = E::load1(a.st, row * (K - 1) + j);
+                    for (int k = 0; k < K; ++k) y = fmaf(w[k], E::load1(xr, t - (K - 1) + k), y);
+                    dy *= silu_grad(y);
                 }
-                v[j] = dpp<0x138>(first, v[kE + j]);
             }
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) later[j] = lane_of(dy, j);
+        }
+        Raw<E> nx, nd;
+        S nh = 0;  // lane j: input j of the K - 1 before the tile, as it lies in memory (converted here, each load was
+                   // waited for: 65 us)
+        const auto load = [&](int64_t k) {
+            const int rem = clamp_tile(a.L - k * kTile);
+            load8<E, VEC>(xr + k * kTile, a.L, rem, lane, nx);
+            load8<E, VEC>(static_cast<const S*>(a.dout) + base + k * kTile, a.L, rem, lane, nd);
+            if (K > 1) {
+                const S* h = k > 0 ? xr + (k * kTile - (K - 1)) : a.st ? static_cast<const S*>(a.st) + row * (K - 1) : nullptr;
+                nh = h ? h[lane < K - 1 ? lane : 0] : 0;
+            }
+        };
+        if (end > first) load(end - 1);
+        for (int64_t k = end - 1; k >= first; --k) {
+            const int64_t t = k * kTile;
+            const int rem = clamp_tile(a.L - t);
+            float v[K - 1 + kE], d[kE + K - 1], o[kE];
+            settle8<E, VEC>(a.L, rem, lane, nx);
+            settle8<E, VEC>(a.L, rem, lane, nd);
+            nx.unpack(v + K - 1);
+            nd.unpack(d);
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) v[j] = dpp<0x138>(lane_of(E::value(nh), j), v[kE + j]);  // wave_shr 1
+            if (k > first) load(k - 1);
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
                 if (SILU) {
                     float y = b;
 #pragma unroll
-                    for (int k = 0; k < K; ++k) y = fmaf(w[k], v[e + k], y);
-                    const float s = fast_rcp(1.0f + fast_exp2(-y * kLog2e));
-                    d[e] *= s * fmaf(y, 1.0f - s, 1.0f);
+                    for (int q = 0; q < K; ++q) y = fmaf(w[q], v[e + q], y);
+                    d[e] *= silu_grad(y);  // past the row's end x and dout are zeros
                 }
-                if (t0 + e >= a.L) d[e] = 0.0f;
                 db += d[e];
 #pragma unroll
-                for (int k = 0; k < K; ++k) dw[k] = fmaf(d[e], v[e + k], dw[k]);
+                for (int q = 0; q < K; ++q) dw[q] = fmaf(d[e], v[e + q], dw[q]);
             }
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
@@ -132,55 +122,97 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(CArgs a) {
             for (int e = 0; e < kE; ++e) {
                 o[e] = 0.0f;
 #pragma unroll
-                for (int k = 0; k < K; ++k) o[e] = fmaf(w[k], d[e + K - 1 - k], o[e]);
-                const int64_t j = t0 + e - (a.L - (K - 1));
-                if (K > 1 && a.dfin && j >= 0 && j < K - 1) o[e] += E::load1(a.dfin, row * (K - 1) + j);
+                for (int q = 0; q < K; ++q) o[e] = fmaf(w[q], d[e + K - 1 - q], o[e]);
             }
-            store8<E, VEC>(a.dx, row, t0, a.L, o);
+            if (K > 1 && a.dfin && t + kTile > a.L - (K - 1)) {  // the row's last K - 1 inputs left as its window
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const int64_t j = t + lane * kE + e - (a.L - (K - 1));
+                    if (j >= 0 && j < K - 1) o[e] += E::load1(a.dfin, row * (K - 1) + j);
+                }
+            }
+            store8<E, VEC>(static_cast<S*>(a.dx) + base + t, rem, lane, o);
         }
-        // `later` now holds dy_0 .. dy_{K-2} (zeros past the row's end)
-        if (K > 1 && a.dst && lane == 0) {
+        // `later` now holds dy_0 .. dy_{K-2} of the row (zeros past its end)
+        if (K > 1 && a.dst && first == 0 && lane == 0) {
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
-                float s = 0.0f;
+                float o = 0.0f;
 #pragma unroll
-                for (int k = 0; k <= j; ++k) s = fmaf(w[k], later[j - k], s);
-                if (a.dfin && j >= a.L) s += E::load1(a.dfin, row * (K - 1) + (j - a.L));
-                E::store1(a.dst, row * (K - 1) + j, s);
+                for (int q = 0; q <= j; ++q) o = fmaf(w[q], later[j - q], o);
+                if (a.dfin && j >= a.L) o += E::load1(a.dfin, row * (K - 1) + (j - a.L));
+                E::store1(a.dst, row * (K - 1) + j, o);
             }
         }
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const float s = wave_sum(dw[k]);
-            if (lane == 0) a.part[k * a.R + row] = s;
+        for (int q = 0; q < K; ++q) s[q] += wave_sum(dw[q]);
+        s[K] += wave_sum(db);
+    };
+    if (a.S > 1) {
+        for (int64_t it = (int64_t)blockIdx.x * 4 + wave; it < items; it += (int64_t)gridDim.x * 4) {
+            float s[K + 1] = {};
+            pass(it / a.S, static_cast<int>(it % a.S), s);
+            if (lane == 0) {
+#pragma unroll
+                for (int q = 0; q <= K; ++q) a.part[q * items + it] = s[q];
+            }
         }
-        db = wave_sum(db);
-        if (lane == 0) a.part[K * a.R + row] = db;
+        return;
+    }
+    const int ways = channel_ways(a.Bt), channels = 4 / ways, lead = wave % ways;
+    for (int64_t c = (int64_t)blockIdx.x * channels; c < a.Dn; c += (int64_t)gridDim.x * channels) {
+        const int64_t ch = c + wave / ways;
+        float s[K + 1] = {};
+        if (ch < a.Dn)
+            for (int64_t b = lead; b < a.Bt; b += ways) pass(b * a.Dn + ch, 0, s);
+        if (lane == 0) {
+#pragma unroll
+            for (int q = 0; q <= K; ++q) sums[wave][q] = s[q];
+        }
+        __syncthreads();
+        if (ch < a.Dn && lead == 0 && lane <= K) {
+            float t = 0.0f;
+            for (int v = 0; v < ways; ++v) t += sums[wave + v][lane];
+            if (lane < K) a.dw[ch * K + lane] = t;
+            else if (a.db) a.db[ch] = t;
+        }
+        __syncthreads();
     }
 }
 
-// The rows of channel d summed in row order.
+// The rows of channel d and their segments summed in order.
 template <int K>
-__global__ __launch_bounds__(256) void conv_sums_kernel(const float* part, float* dw, float* db, int64_t Dn, int64_t n) {
-    const int64_t R = Dn * n;
+__global__ __launch_bounds__(256) void conv_sums_kernel(const float* part, float* dw, float* db, int64_t Dn, int64_t n,
+                                                        int S) {
+    const int64_t items = Dn * n * S;
     for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < Dn * (K + 1);
          g += (int64_t)gridDim.x * blockDim.x) {
         const int64_t d = g % Dn, k = g / Dn;
         float s = 0.0f;
-        for (int64_t b = 0; b < n; ++b) s += part[k * R + b * Dn + d];
+        for (int64_t b = 0; b < n; ++b)
+            for (int j = 0; j < S; ++j) s += part[k * items + (b * Dn + d) * S + j];
         if (k < K) dw[d * K + k] = s;
         else if (db) db[d] = s;
     }
 }
 
-unsigned blocks_for(int64_t n, int64_t per) {
-    const int64_t b = (n + per - 1) / per;
-    return static_cast<unsigned>(b < 1 ? 1 : b > (1 << 22) ? (1 << 22) : b);
+// Segments per row, by sizes alone: enough waves to fill the chip (8192, eight a SIMD), each with a tile.
+struct Plan {
+    int S;
+    int64_t tiles, seg_tiles;
+};
+Plan plan_of(int64_t R, int64_t L) {
+    Plan p;
+    p.tiles = (L + kTile - 1) / kTile;
+    const int64_t want = R > 0 ? (8192 + R - 1) / R : 1;
+    p.seg_tiles = (p.tiles + want - 1) / want;
+    p.S = p.tiles > 0 ? static_cast<int>((p.tiles + p.seg_tiles - 1) / p.seg_tiles) : 1;
+    return p;
 }
 
 template <class E, int K, bool SILU>
 void launch_v(const CArgs& a, bool vec, hipStream_t s) {
-    const dim3 grid(blocks_for(a.R, 4)), block(256);
+    const dim3 grid(a.S > 1 ? blocks_for(a.R * a.S, 4) : blocks_for(a.Dn, 4 / channel_ways(a.Bt))), block(256);
     if (vec) conv_bwd_kernel<E, K, SILU, true><<<grid, block, 0, s>>>(a);
     else conv_bwd_kernel<E, K, SILU, false><<<grid, block, 0, s>>>(a);
 }
@@ -189,7 +221,8 @@ template <class E, int K>
 hipError_t launch_k(const CArgs& a, const ConvBwdLaunch& l, hipStream_t s) {
     if (l.silu) launch_v<E, K, true>(a, l.vec_ok, s);
     else launch_v<E, K, false>(a, l.vec_ok, s);
-    conv_sums_kernel<K><<<dim3(blocks_for(a.Dn * (K + 1), 256)), dim3(256), 0, s>>>(a.part, l.dw, l.db, a.Dn, a.R / a.Dn);
+    if (a.S > 1) conv_sums_kernel<K><<<dim3(blocks_for(a.Dn * (K + 1), 256)), dim3(256), 0, s>>>(a.part, l.dw, l.db, a.Dn, a.R / a.Dn,
+                                                                                  a.S);
     return hipGetLastError();
 }
 
@@ -205,12 +238,18 @@ hipError_t launch_e(const CArgs& a, const ConvBwdLaunch& l, hipStream_t s) {
 
 }  // namespace
 
-int64_t conv1d_bwd_scratch(int64_t Bt, int64_t Dn, int64_t, int64_t K) { return (K + 1) * Bt * Dn; }
+int64_t conv1d_bwd_scratch(int64_t Bt, int64_t Dn, int64_t L, int64_t K) {
+    const int S = plan_of(Bt * Dn, L).S;
+    return S > 1 ? (K + 1) * Bt * Dn * S : 0;
+}
 
 hipError_t launch_conv1d_bwd(const ConvBwdLaunch& l, hipStream_t s) {
+    const Plan p = plan_of(l.R, l.L);
     CArgs a{};
     a.x = l.x; a.w = l.w; a.bias = l.bias; a.st = l.state_in; a.dout = l.dout; a.dfin = l.dfinal; a.dx = l.dx;
-    a.dst = l.dstate; a.part = l.scratch; a.Dn = l.Dn; a.L = l.L; a.R = l.R;
+    a.dst = l.dstate; a.dw = l.dw; a.db = l.db; a.part = l.scratch; a.Dn = l.Dn; a.L = l.L; a.R = l.R;
+    a.Bt = l.R / l.Dn;
+    a.tiles = p.tiles; a.seg_tiles = p.seg_tiles; a.S = p.S;
     return l.bf16 ? launch_e<BF16>(a, l, s) : launch_e<F32>(a, l, s);
 }
 

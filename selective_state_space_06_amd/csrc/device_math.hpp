@@ -71,6 +71,7 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float a) {
 struct F32 {
     using storage = float;
     static constexpr int kPerVec = 4;  // elements per 16-byte vector
+    __device__ static float value(float w) { return w; }
     __device__ static float load1(const void* p, int64_t i) {
         return static_cast<const float*>(p)[i];
     }
@@ -94,6 +95,7 @@ struct F32 {
 struct BF16 {
     using storage = uint16_t;
     static constexpr int kPerVec = 8;
+    __device__ static float value(uint16_t w) { return bf16_to_f32(w); }
     __device__ static float load1(const void* p, int64_t i) {
         return bf16_to_f32(static_cast<const uint16_t*>(p)[i]);
     }

@@ -6,20 +6,22 @@
 //     h_t = a h_{t-1} + m p x_t,    out_t = h_t
 // and backwards, with w_t = dL/dh_{t-1} through step t (w after the last step: dL/d last_state)
 //     G_t = dout_t + w_{t+1},  w_t = a G_t
-//     dx = G m p,  di = G m x p (1 - p),  ds = G (a^2 / m p x - a h_{t-1}),
+//     dx = G m p,  di = G m p x (1 - p),  ds = G (a^2 / m p x - a h_{t-1}),
 //     df = ds s (1 - r),  drate = sum over batch and time of ds r
 // (dm/ds = a^2 / m).  A step is the map h -> a h + v; maps compose as (a, v)(a', v') =
-// (a a', a v' + v), so a wave covers 512 consecutive steps of a row: each lane folds its own eight,
-// an in-wave scan of the lanes' maps gives every lane the state it starts from, and the lane then
-// runs its steps again from there.  The backward scan is the same with time reversed.
+// (a a', a v' + v), so a wave covers 512 consecutive steps of a row (a tile): each lane folds its own
+// eight, an in-wave scan of the lanes' maps gives every lane the state it starts from, and the lane
+// then runs its steps again from there.  The backward scan is the same with time reversed; it starts
+// each tile from the state the forward saved for it.
+#include <algorithm>
+
 #include "device_math.hpp"
 #include "mss_internal.hpp"
+#include "row_io.hpp"
 
 namespace mss {
 namespace {
 
-constexpr int kE = 8;              // steps per lane
-constexpr int kTile = 64 * kE;     // steps per wave and round; also the spacing of saved states
 static_assert(kTile == kGatedTile, "the ABI's saved_states spacing");
 
 struct GArgs {
@@ -31,268 +33,409 @@ struct GArgs {
     const int32_t* lens;    // nullable
     void* out;              // nullable
     float* last;            // nullable
-    float* saved;           // (R, ceil(L / 512)): forward writes (nullable), backward reads
+    float* saved;           // (R, tiles): forward writes (nullable), backward reads
     const void* dout;
     const float* dlast;     // nullable
     void* dx;
     void* df;
     void* di;
-    float* drate_part;      // (R)
+    float* drate;           // (Dn)
+    float* drate_part;      // (R, S), or null: drate is written itself
     float* dh0;             // nullable
-    int64_t Dn, L, R;
+    float2* seg;            // (R, S): the segments' maps, when S > 1
+    int64_t Bt, Dn, L, R, tiles;
+    int64_t seg_tiles;      // tiles per segment
+    int S;                  // segments per row
 };
 
-// What one step needs of its gates.  q = 1 - a^2 = 1 - e^-2s directly loses its digits as s -> 0
-// (a rate of 0.01 leaves two), so below 2s = 1/4 it is the series of 1 - e^-y up to y^6 (the next
-// term is y^6 / 5040 < 5e-8 of it).
-struct Gate {
-    float r, a, m, p, s;
-    float rc, pc;  // 1 - r, 1 - p
+// ---- gates
+// q = 1 - a^2 = 1 - e^-y, y = 2 s, formed as such loses its digits as y -> 0 (a decay of 0.99 leaves
+// five), so up to y = 1/2 it is y (k0 + .. + k4 y^4), the minimax fit of (1 - e^-y) / y there (relative
+// error 7.7e-8, 1.9e-7 with fp32's rounding).
+constexpr float kQ[5] = {0.9999999403953552f, -0.4999924898147583f, 0.16654814779758453f, -0.04100127890706062f,
+                         0.006771037820726633f};
+
+// The rate's share of every step, the same for a whole row.  Rows whose decay stays within the fit
+// (rate < 1/4: every step of them has y < 1/2) take its coefficients in r directly and need neither y
+// nor the other branch (2.8B layer bf16: 65 us against 67 forward, 115 against 122 backward).
+struct Row {
+    float rate, nrl;  // -rate log2 e
+    float c[5];       // kQ[k] (2 rate)^(k + 1)
+    bool small;
 };
-// sigmoid(v) and, without the cancellation of 1 - sigmoid for v >> 0, its complement e^-v sigmoid(v).
-// Where e^-v overflows the product is inf * 0, and the minimum picks its limit, 1.
-__device__ __forceinline__ float sigmoid(float v, float& rest) {
-    const float e = fast_exp2(-v * kLog2e), r = fast_rcp(1.0f + e);
-    rest = fminf(e * r, 1.0f);
-    return r;
+// The least q: keeps 1 / m finite where the gate is closed (r = 0, m = 0; m is then 2^-62, and a normal number,
+// which a reciprocal root takes).
+constexpr float kLeastQ = 0x1p-124f;
+struct True { static constexpr bool value = true; };
+struct False { static constexpr bool value = false; };
+__device__ __forceinline__ Row row_of(float rate) {
+    Row w;
+    w.rate = rate;
+    w.nrl = -rate * kLog2e;
+    w.small = rate < 0.25f && rate > 0.0f;
+    float p = 2.0f * rate;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w.c[k] = kQ[k] * p, p *= 2.0f * rate;
+    return w;
 }
-__device__ __forceinline__ Gate gate_of(float f, float i, float rate) {
-    Gate g;
-    g.r = sigmoid(f, g.rc);
-    g.p = sigmoid(i, g.pc);
-    g.s = rate * g.r;
-    g.a = fast_exp2(-g.s * kLog2e);
-    const float y = 2.0f * g.s;
-    float q = fmaf(y, -1.0f / 6.0f, 1.0f);
-    q = fmaf(y * (-1.0f / 5.0f), q, 1.0f);
-    q = fmaf(y * (-1.0f / 4.0f), q, 1.0f);
-    q = fmaf(y * (-1.0f / 3.0f), q, 1.0f);
-    q = fmaf(y * (-1.0f / 2.0f), q, 1.0f);
-    q = y < 0.25f ? y * q : fmaf(-g.a, g.a, 1.0f);
-    g.m = __builtin_amdgcn_sqrtf(q);
-    return g;
+template <bool SMALL>
+__device__ __forceinline__ float q_of(const Row& w, float r, float a) {
+    if (SMALL) return r * fmaf(r, fmaf(r, fmaf(r, fmaf(r, w.c[4], w.c[3]), w.c[2]), w.c[1]), w.c[0]);
+    const float y = 2.0f * w.rate * r;
+    const float t = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, kQ[4], kQ[3]), kQ[2]), kQ[1]), kQ[0]);
+    return y < 0.5f ? t : fmaf(-a, a, 1.0f);
 }
+__device__ __forceinline__ float exp_neg(float v) { return fast_exp2(v * -kLog2e); }
 
-// Eight consecutive elements from step t0 of a row of L (zeros past the end).  VEC: rows are whole
-// aligned 16-byte vectors; otherwise element-aligned 16-byte accesses and the row's last, partial
-// vector element by element.
-template <class E, bool VEC>
-__device__ __forceinline__ void load8(const void* base, int64_t row, int64_t t0, int64_t L, float* v) {
-    constexpr int V = E::kPerVec;
-    const auto* p = static_cast<const typename E::storage*>(base) + row * L;
-#pragma unroll
-    for (int j = 0; j < kE / V; ++j) {
-        const int64_t t = t0 + j * V;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (t + V <= L) {
-            if (VEC) w = *reinterpret_cast<const uint4*>(p + t);
-            else __builtin_memcpy(&w, p + t, 16);
-            E::unpack(w, v + j * V);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[j * V + e] = (!VEC && t + e < L) ? E::load1(p, t + e) : 0.0f;
-        }
-    }
-}
-template <class E, bool VEC>
-__device__ __forceinline__ void store8(void* base, int64_t row, int64_t t0, int64_t L, const float* v) {
-    constexpr int V = E::kPerVec;
-    auto* p = static_cast<typename E::storage*>(base) + row * L;
-#pragma unroll
-    for (int j = 0; j < kE / V; ++j) {
-        const int64_t t = t0 + j * V;
-        const uint4 w = E::pack(v + j * V);
-        if (t + V <= L) {
-            if (VEC) *reinterpret_cast<uint4*>(p + t) = w;
-            else __builtin_memcpy(p + t, &w, 16);
-        } else if (!VEC) {
-#pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (t + e < L) E::store1(p, t + e, v[j * V + e]);
-        }
-    }
-}
-
-// v of the lane CTRL names (a DPP move), `old` where there is none.
+// ---- scans over the lanes
+// One round of a scan: the map of the lane CTRL names applied before this lane's.
 template <int CTRL, int ROWS = 0xF>
-__device__ __forceinline__ float dpp(float old, float v) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(v), CTRL, ROWS, 0xF, false));
+__device__ __forceinline__ void join(float& P, float& H) {
+    const float p = dpp<CTRL, ROWS>(1.0f, P), h = dpp<CTRL, ROWS>(0.0f, H);
+    H = fmaf(P, h, H);
+    P *= p;
 }
-__device__ __forceinline__ float lane_of(float v, int lane) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
-
 // Inclusive scan of the lanes' maps in lane order: lane l ends with the composition of lanes 0 .. l.
 __device__ __forceinline__ void scan_up(float& P, float& H) {
-#define MSS_STEP(CTRL, ROWS)                       \
-    {                                              \
-        const float p = dpp<CTRL, ROWS>(1.0f, P);  \
-        const float h = dpp<CTRL, ROWS>(0.0f, H);  \
-        H = fmaf(P, h, H);                         \
-        P *= p;                                    \
-    }
-    MSS_STEP(0x111, 0xF)  // row_shr 1, 2, 4, 8: within the 16-lane rows
-    MSS_STEP(0x112, 0xF)
-    MSS_STEP(0x114, 0xF)
-    MSS_STEP(0x118, 0xF)
-    MSS_STEP(0x142, 0xA)  // row_bcast 15 into rows 1 and 3, then row_bcast 31 into rows 2 and 3
-    MSS_STEP(0x143, 0xC)
+    join<0x111>(P, H);  // row_shr 1, 2, 4, 8: within the 16-lane rows
+    join<0x112>(P, H);
+    join<0x114>(P, H);
+    join<0x118>(P, H);
+    join<0x142, 0xA>(P, H);  // row_bcast 15 into rows 1 and 3, then row_bcast 31 into rows 2 and 3
+    join<0x143, 0xC>(P, H);
 }
-// The same from the last lane down, applied to the value w that enters after lane 63: returns what
-// enters the lane's own map, and leaves in w what leaves lane 0.
-__device__ __forceinline__ float scan_down(float P, float W, float& w, int lane) {
-#define MSS_STEP_DOWN(CTRL)                 \
-    {                                       \
-        const float p = dpp<CTRL>(1.0f, P); \
-        const float h = dpp<CTRL>(0.0f, W); \
-        W = fmaf(P, h, W);                  \
-        P *= p;                             \
-    }
-    MSS_STEP_DOWN(0x101)  // row_shl 1, 2, 4, 8
-    MSS_STEP_DOWN(0x102)
-    MSS_STEP_DOWN(0x104)
-    MSS_STEP_DOWN(0x108)
-    // each row's whole map sits in its first lane
-    const float w3 = w;
-    const float w2 = fmaf(lane_of(P, 48), w3, lane_of(W, 48));
-    const float w1 = fmaf(lane_of(P, 32), w2, lane_of(W, 32));
-    const float w0 = fmaf(lane_of(P, 16), w1, lane_of(W, 16));
-    w = fmaf(lane_of(P, 0), w0, lane_of(W, 0));
-    const float in = lane < 16 ? w0 : lane < 32 ? w1 : lane < 48 ? w2 : w3;
-    const float p = dpp<0x101>(1.0f, P), h = dpp<0x101>(0.0f, W);
-    return fmaf(p, in, h);
-#undef MSS_STEP
-#undef MSS_STEP_DOWN
+// What enters lane l's map after an inclusive scan when h enters lane 0's.
+__device__ __forceinline__ float enter_up(float P, float H, float h) {
+    return fmaf(dpp<0x138>(1.0f, P), h, dpp<0x138>(0.0f, H));  // wave_shr 1
 }
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+// The same from the last lane down.  The wave's whole map ends in (P0, W0), and rp, rw hold the map
+// of the 16-lane rows after the lane's.
+struct Down {
+    float P, W;    // inclusive within the row
+    float rp, rw;  // of the rows after this lane's
+    float P0, W0;
+};
+__device__ __forceinline__ Down scan_down(float P, float W, int lane) {
+    join<0x101>(P, W);  // row_shl 1, 2, 4, 8
+    join<0x102>(P, W);
+    join<0x104>(P, W);
+    join<0x108>(P, W);
+    const float p3 = lane_of(P, 48), w3 = lane_of(W, 48);
+    const float p2 = lane_of(P, 32), w2 = lane_of(W, 32);
+    const float p1 = lane_of(P, 16), w1 = lane_of(W, 16);
+    const float q2 = p2 * p3, v2 = fmaf(p2, w3, w2);
+    const float q1 = p1 * q2, v1 = fmaf(p1, v2, w1);
+    Down d;
+    d.P = P;
+    d.W = W;
+    d.rp = lane < 16 ? q1 : lane < 32 ? q2 : lane < 48 ? p3 : 1.0f;
+    d.rw = lane < 16 ? v1 : lane < 32 ? v2 : lane < 48 ? w3 : 0.0f;
+    d.P0 = lane_of(P, 0) * q1;
+    d.W0 = fmaf(lane_of(P, 0), v1, lane_of(W, 0));
+    return d;
 }
-
+// What enters lane l's map when w enters lane 63's.
+__device__ __forceinline__ float enter_down(const Down& d, float w) {
+    const float row = fmaf(d.rp, w, d.rw);
+    return fmaf(dpp<0x101>(1.0f, d.P), row, dpp<0x101>(0.0f, d.W));
+}
 __device__ __forceinline__ int64_t length_of(const GArgs& a, int64_t row) {
     if (!a.lens) return a.L;
     const int64_t n = a.lens[row / a.Dn];
     return n < 0 ? 0 : n > a.L ? a.L : n;
 }
 
-// One wave per row, tile after tile.
-template <class E, bool VEC>
-__global__ __launch_bounds__(256) void gated_fwd_kernel(GArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t tiles = (a.L + kTile - 1) / kTile;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.R; row += (int64_t)gridDim.x * 4) {
-        const int64_t len = length_of(a, row);
-        const float rate = a.rate[row % a.Dn];
-        float h = a.h0 ? a.h0[row] : 0.0f;
-        for (int64_t k = 0; k < tiles; ++k) {
-            if (a.saved && lane == 0) a.saved[row * tiles + k] = h;
-            const int64_t t0 = k * kTile + lane * kE;
-            float x[kE], f[kE], i[kE], av[kE], vv[kE];
-            load8<E, VEC>(a.x, row, t0, a.L, x);
-            load8<E, VEC>(a.f, row, t0, a.L, f);
-            load8<E, VEC>(a.i, row, t0, a.L, i);
-            float P = 1.0f, H = 0.0f;
+// Who does what.  W waves share a row, W tiles a round, and hand their maps on through LDS; with W = 1 a
+// block of four waves holds four rows.  With S > 1 a row is cut into S segments of whole rounds, and
+// a work item is a (row, segment).
+template <int W>
+struct Place {
+    static constexpr int kRows = W == 1 ? 4 : 1;              // work items per block
+    static constexpr int kThreads = W == 1 ? 256 : 64 * W;
+    int lane, wave, item;
+    __device__ __forceinline__ Place() {
+        lane = threadIdx.x & 63;
+        const int v = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+        wave = W == 1 ? 0 : v;
+        item = W == 1 ? v : 0;
+    }
+};
+
+// The maps of a round's W tiles joined through LDS (two buffers in turn: a wave may enter the next round
+// while another still reads this one's).  In: this wave's map.  Out: the map of the waves before it in
+// order (UP) or after it (!UP), and of all of them.
+template <int W, bool UP>
+__device__ __forceinline__ void join_waves(float2 (*sh)[W], int64_t round, const Place<W>& at, float P, float H,
+                                           float2& mine, float2& all) {
+    float2* buf = sh[round & 1];
+    if (at.lane == 0) buf[at.wave] = make_float2(P, H);
+    __syncthreads();
+    mine = all = make_float2(1.0f, 0.0f);
 #pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                const Gate g = gate_of(f[e], i[e], rate);
-                const bool on = t0 + e < len;
-                av[e] = on ? g.a : 1.0f;
-                vv[e] = on ? g.m * g.p * x[e] : 0.0f;
-                H = fmaf(av[e], H, vv[e]);
-                P *= av[e];
-            }
-            scan_up(P, H);
-            const float p = dpp<0x138>(1.0f, P), q = dpp<0x138>(0.0f, H);  // wave_shr 1
-            float s = fmaf(p, h, q);
-            h = fmaf(lane_of(P, 63), h, lane_of(H, 63));
-            if (a.out) {
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    s = fmaf(av[e], s, vv[e]);
-                    vv[e] = t0 + e < len ? s : 0.0f;
-                }
-                store8<E, VEC>(a.out, row, t0, a.L, vv);
-            }
-        }
-        if (a.last && lane == 0) a.last[row] = h;
+    for (int k = 0; k < W; ++k) {
+        const int v = UP ? k : W - 1 - k;
+        if (v == at.wave) mine = all;
+        const float2 m = buf[v];
+        all = make_float2(all.x * m.x, fmaf(m.x, all.y, m.y));
     }
 }
 
-// One wave per row, tiles from the last to the first; each tile's forward states are run again
-// from the saved state it starts with.
-template <class E, bool VEC>
-__global__ __launch_bounds__(256) void gated_bwd_kernel(GArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t tiles = (a.L + kTile - 1) / kTile;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); row < a.R; row += (int64_t)gridDim.x * 4) {
+// ---- forward.  FOLD: only the segments' maps are wanted (nothing is written but a.seg).
+template <class E, bool VEC, int W, bool FOLD>
+__global__ __launch_bounds__(Place<W>::kThreads) void gated_fwd_kernel(GArgs a) {
+    using S = typename E::storage;
+    __shared__ float2 sh[2][W];
+    const Place<W> at;
+    const int64_t items = a.R * a.S;
+    for (int64_t it = (int64_t)blockIdx.x * Place<W>::kRows + at.item; it < items;
+         it += (int64_t)gridDim.x * Place<W>::kRows) {
+        const int64_t row = a.S == 1 ? it : it / a.S;
+        const int seg = a.S == 1 ? 0 : static_cast<int>(it % a.S);
+        const int64_t first = seg * a.seg_tiles;
+        const int64_t end = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
         const int64_t len = length_of(a, row);
-        const float rate = a.rate[row % a.Dn];
-        float w = a.dlast ? a.dlast[row] : 0.0f;
-        float drate = 0.0f;
-        for (int64_t k = tiles - 1; k >= 0; --k) {
-            const int64_t t0 = k * kTile + lane * kE;
-            const float h = a.saved[row * tiles + k];
-            float x[kE], f[kE], i[kE], d[kE], before[kE];
-            Gate g[kE];
-            load8<E, VEC>(a.x, row, t0, a.L, x);
-            load8<E, VEC>(a.f, row, t0, a.L, f);
-            load8<E, VEC>(a.i, row, t0, a.L, i);
-            load8<E, VEC>(a.dout, row, t0, a.L, d);
-            float P = 1.0f, H = 0.0f;
-#pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                g[e] = gate_of(f[e], i[e], rate);
-                if (t0 + e >= len) {  // a step past the end: the identity, and no gradient
-                    g[e].a = 1.0f;
-                    g[e].m = g[e].s = g[e].p = g[e].r = 0.0f;
-                    x[e] = d[e] = 0.0f;
-                }
-                H = fmaf(g[e].a, H, g[e].m * g[e].p * x[e]);
-                P *= g[e].a;
-            }
-            const float Pl = P;
+        const Row w = row_of(a.rate[row % a.Dn]);
+        float h = !FOLD && a.h0 ? a.h0[row] : 0.0f, all_p = 1.0f;
+        if (!FOLD && seg > 0) {  // the segments before this one, a lane each
+            const float2 m = at.lane < seg ? a.seg[row * a.S + at.lane] : make_float2(1.0f, 0.0f);
+            float P = m.x, H = m.y;
             scan_up(P, H);
-            float s = fmaf(dpp<0x138>(1.0f, P), h, dpp<0x138>(0.0f, H));
-            float W = 0.0f;
+            h = fmaf(lane_of(P, 63), h, lane_of(H, 63));
+        }
+        const auto x_ = static_cast<const S*>(a.x) + row * a.L, f_ = static_cast<const S*>(a.f) + row * a.L;
+        const auto i_ = static_cast<const S*>(a.i) + row * a.L;
+        Raw<E> nx{}, nf{}, ni{};  // the next tile's inputs, on their way while this one is computed
+        const auto load = [&](int64_t k) {
+            const int64_t t = k * kTile;
+            const int rem = clamp_tile(len - t);  // nothing past the sequence's end is read...
+            if (rem > 0) {
+                const int in = rem == kTile ? kTile : clamp_tile(a.L - t);  // ...but whole vectors of the row
+                load8<E, VEC>(f_ + t, a.L, in, at.lane, nf);
+                load8<E, VEC>(i_ + t, a.L, in, at.lane, ni);
+                load8<E, VEC>(x_ + t, a.L, in, at.lane, nx);
+            }
+        };
+        load(first + at.wave);
+        // A round of W tiles from tile k0.  FAST: every step of it lies inside the sequence, and w.small.
+        const auto round = [&](int64_t k0, auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
+            const int64_t k = k0 + at.wave, t = k * kTile;
+            const int on = FAST ? kTile : k < end ? clamp_tile(len - t) : 0;  // this tile's steps in the sequence
+            const int rem = FAST ? kTile : k < end ? clamp_tile(a.L - t) : 0;
+            float v[kE], f[kE], i[kE], P = 1.0f, H = 0.0f;
+            if (!FAST) {
+                settle8<E, VEC>(a.L, rem, at.lane, nf);
+                settle8<E, VEC>(a.L, rem, at.lane, ni);
+                settle8<E, VEC>(a.L, rem, at.lane, nx);
+            }
+            nf.unpack(f);
+            ni.unpack(i);
+            nx.unpack(v);
+            if (k0 + W < end) load(k + W);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {  // f becomes a, v the input term
+                const float r = fast_rcp(1.0f + exp_neg(f[e])), p = fast_rcp(1.0f + exp_neg(i[e]));
+                f[e] = fast_exp2(r * w.nrl);
+                v[e] *= __builtin_amdgcn_sqrtf(q_of<FAST>(w, r, f[e])) * p;
+                if (!FAST && at.lane * kE + e >= on) f[e] = 1.0f, v[e] = 0.0f;
+                H = fmaf(f[e], H, v[e]);
+                P *= f[e];
+            }
+            scan_up(P, H);
+            float start = h;
+            if (W == 1) {
+                if (FOLD) all_p *= lane_of(P, 63);
+                h = fmaf(lane_of(P, 63), h, lane_of(H, 63));
+            } else {
+                float2 mine, all;
+                join_waves<W, true>(sh, k0 / W, at, lane_of(P, 63), lane_of(H, 63), mine, all);
+                start = fmaf(mine.x, h, mine.y);
+                if (FOLD) all_p *= all.x;
+                h = fmaf(all.x, h, all.y);
+            }
+            if (FOLD || rem == 0) return;
+            if (a.saved && at.lane == 0) a.saved[row * a.tiles + k] = start;
+            if (!a.out) return;
+            float s = enter_up(P, H, start);
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
-                before[e] = s;
-                s = fmaf(g[e].a, s, g[e].m * g[e].p * x[e]);
+                s = fmaf(f[e], s, v[e]);
+                v[e] = FAST || at.lane * kE + e < on ? s : 0.0f;
+            }
+            store8<E, VEC>(static_cast<S*>(a.out) + row * a.L + t, rem, at.lane, v);
+        };
+        const int64_t inside = w.small ? len / kTile : 0;  // tiles a fast round may end at
+        for (int64_t k0 = first; k0 < end; k0 += W) {
+            if (k0 + W <= inside && k0 + W <= end) round(k0, True{});
+            else round(k0, False{});
+        }
+        if (at.lane == 0 && at.wave == 0) {
+            if (FOLD) a.seg[it] = make_float2(all_p, h);
+            else if (a.last && end == a.tiles) a.last[row] = h;
+        }
+        if (W > 1) __syncthreads();  // the next item's first round writes the buffer this one's last may read
+    }
+}
+
+// ---- backward.  FOLD: only the segments' maps are wanted; they need the decays and dout alone.
+template <class E, bool VEC, int W, bool FOLD>
+__global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gated_bwd_kernel(GArgs a) {
+    using S = typename E::storage;
+    __shared__ float2 sh[2][W];
+    __shared__ float sums[W == 1 ? 4 : W];
+    const Place<W> at;
+    // One row's segment; returns this wave's share of its part of drate.
+    const auto pass = [&](int64_t row, int seg) {
+        const int64_t first = seg * a.seg_tiles;
+        const int64_t end = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
+        const int64_t len = length_of(a, row);
+        const Row w = row_of(a.rate[row % a.Dn]);
+        float g = !FOLD && a.dlast ? a.dlast[row] : 0.0f, all_p = 1.0f, drate = 0.0f;
+        if (!FOLD && seg < a.S - 1) {  // the segments after this one, a lane each, the last one first
+            const float2 m = at.lane < a.S - 1 - seg ? a.seg[row * a.S + a.S - 1 - at.lane] : make_float2(1.0f, 0.0f);
+            float P = m.x, H = m.y;
+            scan_up(P, H);
+            g = fmaf(lane_of(P, 63), g, lane_of(H, 63));
+        }
+        const auto round = [&](int64_t k0, auto fast) {
+            constexpr bool FAST = decltype(fast)::value;
+            const int64_t k = k0 + at.wave, t = k * kTile, p0 = row * a.L + t;
+            const int on = FAST ? kTile : k < end ? clamp_tile(len - t) : 0;  // this tile's steps in the sequence
+            const int rem = FAST ? kTile : k < end ? clamp_tile(a.L - t) : 0;
+            Raw<E> rf{}, rd{}, rx{}, ri{};
+            float start = 0.0f;
+            if (on > 0) {
+                load8<E, VEC>(static_cast<const S*>(a.f) + p0, a.L, rem, at.lane, rf);
+                load8<E, VEC>(static_cast<const S*>(a.dout) + p0, a.L, rem, at.lane, rd);
+                if (!FOLD) {
+                    load8<E, VEC>(static_cast<const S*>(a.i) + p0, a.L, rem, at.lane, ri);
+                    load8<E, VEC>(static_cast<const S*>(a.x) + p0, a.L, rem, at.lane, rx);
+                    start = a.saved[row * a.tiles + k];
+                }
+            }
+            if (!FAST) {
+                settle8<E, VEC>(a.L, rem, at.lane, rf);
+                settle8<E, VEC>(a.L, rem, at.lane, rd);
+                if (!FOLD) {
+                    settle8<E, VEC>(a.L, rem, at.lane, ri);
+                    settle8<E, VEC>(a.L, rem, at.lane, rx);
+                }
+            }
+            // of every step: a, r, s (1 - r), a^2 p x / m, p m, x (1 - p), p m x, dout: no more of them than the
+            // second pass needs, so that four waves share a SIMD (2.8B layer bf16: 115 us, 120 at three)
+            float av[kE], rv[kE], sc[kE], into[kE], pm[kE], xc[kE], v[kE], d[kE];
+            float P = 1.0f, H = 0.0f, V = 0.0f;
+            rf.unpack(rv);
+            rd.unpack(d);
+            if (!FOLD) {
+                ri.unpack(pm);
+                rx.unpack(xc);
             }
 #pragma unroll
-            for (int e = kE - 1; e >= 0; --e) W = g[e].a * (d[e] + W);
-            float wt = scan_down(Pl, W, w, lane);
+            for (int e = 0; e < kE; ++e) {
+                const bool off = !FAST && at.lane * kE + e >= on;
+                const float ef = exp_neg(rv[e]);
+                rv[e] = fast_rcp(1.0f + ef);
+                av[e] = fast_exp2(rv[e] * w.nrl);
+                if (!FOLD) {
+                    // 1 - sigmoid without its cancellation; where e^-f overflows the product is inf * 0 and the
+                    // minimum picks its limit, 1
+                    const float x = xc[e], ei = exp_neg(pm[e]), p = fast_rcp(1.0f + ei);
+                    const float q = fmaxf(q_of<FAST>(w, rv[e], av[e]), kLeastQ);
+                    float im = __builtin_amdgcn_rsqf(q);  // 1 / m
+                    if (!FAST) im = w.rate == 0.0f ? 0.0f : im;
+                    sc[e] = w.rate * rv[e] * fminf(ef * rv[e], 1.0f);
+                    xc[e] = x * fminf(ei * p, 1.0f);
+                    into[e] = av[e] * av[e] * im * (p * x);
+                    pm[e] = p * (q * im);
+                    v[e] = pm[e] * x;
+                    if (off) rv[e] = sc[e] = xc[e] = into[e] = pm[e] = v[e] = 0.0f;
+                }
+                if (off) av[e] = 1.0f, d[e] = 0.0f;
+                P *= av[e];
+                if (!FOLD) H = fmaf(av[e], H, v[e]);
+            }
+#pragma unroll
+            for (int e = kE - 1; e >= 0; --e) V = av[e] * (d[e] + V);
+            const Down down = scan_down(P, V, at.lane);
+            float in = g;  // what enters this tile from the later ones
+            if (W == 1) {
+                if (FOLD) all_p *= down.P0;
+                g = fmaf(down.P0, g, down.W0);
+            } else {
+                float2 mine, all;
+                join_waves<W, false>(sh, k0 / W, at, down.P0, down.W0, mine, all);
+                in = fmaf(mine.x, g, mine.y);
+                if (FOLD) all_p *= all.x;
+                g = fmaf(all.x, g, all.y);
+            }
+            if (FOLD || rem == 0) return;
+            scan_up(P, H);
+            float s = enter_up(P, H, start), wt = enter_down(down, in);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                into[e] = fmaf(-av[e], s, into[e]);  // ds / G
+                s = fmaf(av[e], s, v[e]);
+            }
 #pragma unroll
             for (int e = kE - 1; e >= 0; --e) {
-                const float G = d[e] + wt;
-                wt = g[e].a * G;
-                const float mp = g[e].m * g[e].p;
-                const float im = g[e].m > 0.0f ? g[e].a * g[e].a * fast_rcp(g[e].m) : 0.0f;
-                const float ds = G * fmaf(-g[e].a, before[e], im * g[e].p * x[e]);
-                d[e] = G * mp;                                   // dx
-                i[e] = G * mp * x[e] * g[e].pc;                  // di
-                f[e] = ds * g[e].s * g[e].rc;                    // df
-                drate = fmaf(ds, g[e].r, drate);
+                const bool off = !FAST && at.lane * kE + e >= on;
+                const float G = d[e] + wt, ds = G * into[e];
+                wt = av[e] * G;
+                pm[e] = off ? 0.0f : pm[e] * G;     // dx
+                xc[e] = off ? 0.0f : xc[e] * pm[e]; // di
+                sc[e] = off ? 0.0f : sc[e] * ds;    // df
+                drate += off ? 0.0f : ds * rv[e];
             }
-            store8<E, VEC>(a.dx, row, t0, a.L, d);
-            store8<E, VEC>(a.di, row, t0, a.L, i);
-            store8<E, VEC>(a.df, row, t0, a.L, f);
+            store8<E, VEC>(static_cast<S*>(a.dx) + p0, rem, at.lane, pm);
+            store8<E, VEC>(static_cast<S*>(a.di) + p0, rem, at.lane, xc);
+            store8<E, VEC>(static_cast<S*>(a.df) + p0, rem, at.lane, sc);
+        };
+        const int64_t inside = w.small ? len / kTile : 0;  // tiles a fast round may end at
+        for (int64_t k0 = first + (end - first - 1) / W * W; k0 >= first; k0 -= W) {
+            if (k0 + W <= inside && k0 + W <= end) round(k0, True{});
+            else round(k0, False{});
         }
-        drate = wave_sum(drate);
-        if (lane == 0) {
-            a.drate_part[row] = drate;
-            if (a.dh0) a.dh0[row] = w;
+        if (at.lane == 0 && at.wave == 0) {
+            if (FOLD) a.seg[row * a.S + seg] = make_float2(all_p, g);
+            else if (a.dh0 && first == 0) a.dh0[row] = g;
+        }
+        return FOLD ? 0.0f : wave_sum(drate);
+    };
+    // the waves' parts added in order, for the wave that leads `ways` of them
+    const auto total = [&](int wave, int ways, float part) {
+        if (ways == 1) return part;
+        if (at.lane == 0) sums[wave] = part;
+        __syncthreads();
+        float s = 0.0f;
+        for (int v = 0; v < ways; ++v) s += sums[wave / ways * ways + v];
+        __syncthreads();
+        return s;
+    };
+    if (W == 1) {
+        const int ways = channel_ways(a.Bt), channels = 4 / ways, lead = at.item % ways;
+        for (int64_t c = (int64_t)blockIdx.x * channels; c < a.Dn; c += (int64_t)gridDim.x * channels) {
+            const int64_t ch = c + at.item / ways;
+            float part = 0.0f;
+            if (ch < a.Dn)
+                for (int64_t b = lead; b < a.Bt; b += ways) part += pass(b * a.Dn + ch, 0);
+            part = total(at.item, ways, part);
+            if (ch < a.Dn && lead == 0 && at.lane == 0) a.drate[ch] = part;
+        }
+    } else {
+        for (int64_t it = blockIdx.x; it < a.R * a.S; it += gridDim.x) {
+            const float part = total(at.wave, W, pass(it / a.S, static_cast<int>(it % a.S)));
+            if (!FOLD && at.lane == 0 && at.wave == 0) (a.drate_part ? a.drate_part : a.drate)[it] = part;
         }
     }
 }
 
-// drate[d] = sum of the rows of channel d, in row order.
-__global__ __launch_bounds__(256) void gated_rate_kernel(const float* part, float* drate, int64_t Dn, int64_t n) {
+// drate[d] = sum over the rows of channel d and their segments, in order.
+__global__ __launch_bounds__(256) void gated_rate_kernel(const float* part, float* drate, int64_t Dn, int64_t Bt, int S) {
     for (int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; d < Dn; d += (int64_t)gridDim.x * blockDim.x) {
         float s = 0.0f;
-        for (int64_t b = 0; b < n; ++b) s += part[b * Dn + d];
+        for (int64_t b = 0; b < Bt; ++b)
+            for (int k = 0; k < S; ++k) s += part[(b * Dn + d) * S + k];
         drate[d] = s;
     }
 }
@@ -300,58 +443,129 @@ __global__ __launch_bounds__(256) void gated_rate_kernel(const float* part, floa
 template <class E>
 __global__ __launch_bounds__(256) void gated_step_kernel(float* state, const void* x, const void* f, const void* i,
                                                          const float* rate, void* out, int64_t Dn, int64_t R) {
-    for (int64_t r = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; r < R; r += (int64_t)gridDim.x * blockDim.x) {
-        const Gate g = gate_of(E::load1(f, r), E::load1(i, r), rate[r % Dn]);
-        const float h = fmaf(g.a, state[r], g.m * g.p * E::load1(x, r));
-        state[r] = h;
-        E::store1(out, r, h);
+    for (int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; n < R; n += (int64_t)gridDim.x * blockDim.x) {
+        const Row w = row_of(rate[n % Dn]);
+        const float r = fast_rcp(1.0f + exp_neg(E::load1(f, n))), p = fast_rcp(1.0f + exp_neg(E::load1(i, n)));
+        const float av = fast_exp2(r * w.nrl);
+        const float m = __builtin_amdgcn_sqrtf(q_of<false>(w, r, av));
+        const float h = fmaf(av, state[n], m * p * E::load1(x, n));
+        state[n] = h;
+        E::store1(out, n, h);
     }
 }
 
-unsigned blocks_for(int64_t n, int64_t per) {
-    const int64_t b = (n + per - 1) / per;
-    return static_cast<unsigned>(b < 1 ? 1 : b > (1 << 22) ? (1 << 22) : b);
+// Waves and segments per row, by sizes alone (so scratch can be named without a device).
+struct Plan {
+    int W, S;
+    int64_t tiles, seg_tiles;
+    // whether the backward leaves parts of drate for a second kernel to add up
+    bool parts(int64_t Bt) const { return S > 1 || (W > 1 && Bt > 1); }
+};
+// Four waves to a row read it in longer runs and hand the map on; they pay where a row has at least two
+// rounds for them (bf16) or one (f32, whose rounds move twice the bytes).  Rows of 16-bit elements that
+// are no whole vectors hold more registers and stay with one wave while there are waves enough.  With
+// few rows a row's waves are all the waves there are: eight, and below 128 rows segments too, whose maps
+// cost a launch and a second reading.  Microseconds, forward / backward (rows x steps):
+//                          one wave      four          eight
+//   20480 x  2048 bf16    66.5 / 111    69.0 / 125
+//   20480 x  4096 bf16     127 / 224     125 / 216     174 / 274
+//   20480 x  4095 bf16     150 / 248     155 / 302     219 / 509
+//   20480 x  2048 f32      126 / 233     114 / 205
+//    4608 x  8192 bf16    64.4 / 121    57.1 / 103    66.0 / 113
+//    1536 x 131072 bf16    370 / 632     368 / 588     315 / 563
+//     512 x 32768 f32     82.3 / 201    52.1 / 98.9   49.9 / 96.5
+//      64 x 131072 f32     296 / 488    93.2 / 169    95.1 / 137    four, eight segments: 42.7 / 58.4
+Plan plan_of(int64_t R, int64_t L, bool bf16, bool vec) {
+    Plan p;
+    p.tiles = (L + kTile - 1) / kTile;
+    p.W = p.tiles >= (bf16 ? 8 : 4) && (R <= 4096 || vec || !bf16) ? 4 : 1;
+    p.S = 1;
+    if (R <= 1024 && p.tiles > 1) p.W = 4;
+    if (R <= 2048 && p.tiles >= 64) p.W = 8;
+    if (R <= 128 && p.tiles >= 128) {
+        p.W = 4;
+        p.S = static_cast<int>(512 / R < 64 ? 512 / R : 64);
+    }
+    // whole rounds per segment, and as many segments as that leaves
+    const int64_t rounds = (p.tiles + p.W - 1) / p.W;
+    p.seg_tiles = (rounds + p.S - 1) / p.S * p.W;
+    p.S = p.tiles > 0 ? static_cast<int>((p.tiles + p.seg_tiles - 1) / p.seg_tiles) : 1;
+    return p;
 }
 
-GArgs args_of(const GatedLaunch& l) {
+GArgs args_of(const GatedLaunch& l, const Plan& p) {
     GArgs a{};
     a.x = l.x; a.f = l.f; a.i = l.i; a.rate = l.rate; a.h0 = l.h0; a.lens = l.lens; a.out = l.out;
     a.last = l.last_state; a.saved = l.saved; a.dout = l.dout; a.dlast = l.dlast; a.dx = l.dx; a.df = l.df;
-    a.di = l.di; a.drate_part = l.scratch; a.dh0 = l.dh0; a.Dn = l.Dn; a.L = l.L; a.R = l.Bt * l.Dn;
+    a.di = l.di; a.dh0 = l.dh0; a.Dn = l.Dn; a.L = l.L; a.R = l.Bt * l.Dn;
+    a.Bt = l.Bt; a.drate = l.drate;
+    a.tiles = p.tiles; a.seg_tiles = p.seg_tiles; a.S = p.S;
+    a.seg = reinterpret_cast<float2*>(l.scratch);  // R S maps when S > 1, then R S parts of drate
+    a.drate_part = p.parts(l.Bt) ? l.scratch + (p.S > 1 ? 2 * a.R * p.S : 0) : nullptr;
     return a;
+}
+
+template <class E, bool VEC, int W>
+void run_w(const GArgs& a, bool bwd, hipStream_t s) {
+    const dim3 grid(blocks_for(a.R * a.S, Place<W>::kRows)), block(Place<W>::kThreads);
+    if (bwd) {
+        if constexpr (W == 1) {
+            const dim3 channels(blocks_for(a.Dn, 4 / channel_ways(a.Bt)));
+            gated_bwd_kernel<E, VEC, 1, false><<<channels, block, 0, s>>>(a);
+        } else {
+            if (a.S > 1) gated_bwd_kernel<E, VEC, W, true><<<grid, block, 0, s>>>(a);
+            gated_bwd_kernel<E, VEC, W, false><<<grid, block, 0, s>>>(a);
+        }
+    } else {
+        if constexpr (W > 1)
+            if (a.S > 1) gated_fwd_kernel<E, VEC, W, true><<<grid, block, 0, s>>>(a);
+        gated_fwd_kernel<E, VEC, W, false><<<grid, block, 0, s>>>(a);
+    }
+}
+template <class E, bool VEC>
+void run_v(const GArgs& a, int W, bool bwd, hipStream_t s) {
+    if (W == 1) run_w<E, VEC, 1>(a, bwd, s);
+    else if (W == 4) run_w<E, VEC, 4>(a, bwd, s);
+    else run_w<E, VEC, 8>(a, bwd, s);
+}
+hipError_t run(const GatedLaunch& l, bool bwd, hipStream_t s) {
+    if (l.Bt * l.Dn == 0) {  // no rows: drate alone is written, with zeros
+        if (bwd) gated_rate_kernel<<<dim3(blocks_for(l.Dn, 256)), dim3(256), 0, s>>>(nullptr, l.drate, l.Dn, 0, 1);
+        return hipGetLastError();
+    }
+    const Plan p = plan_of(l.Bt * l.Dn, l.L, l.bf16, l.vec_ok);
+    const GArgs a = args_of(l, p);
+    {
+        if (l.bf16) l.vec_ok ? run_v<BF16, true>(a, p.W, bwd, s) : run_v<BF16, false>(a, p.W, bwd, s);
+        else l.vec_ok ? run_v<F32, true>(a, p.W, bwd, s) : run_v<F32, false>(a, p.W, bwd, s);
+    }
+    if (bwd && a.drate_part)
+        gated_rate_kernel<<<dim3(blocks_for(a.Dn, 256)), dim3(256), 0, s>>>(a.drate_part, l.drate, a.Dn, l.Bt, p.S);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-int64_t gated_fwd_scratch(int64_t, int64_t, int64_t) { return 0; }
-int64_t gated_bwd_scratch(int64_t Bt, int64_t Dn, int64_t) { return Bt * Dn; }
-
-hipError_t launch_gated_fwd(const GatedLaunch& l, hipStream_t s) {
-    const GArgs a = args_of(l);
-    const dim3 grid(blocks_for(a.R, 4)), block(256);
-    if (l.bf16) {
-        if (l.vec_ok) gated_fwd_kernel<BF16, true><<<grid, block, 0, s>>>(a);
-        else gated_fwd_kernel<BF16, false><<<grid, block, 0, s>>>(a);
-    } else {
-        if (l.vec_ok) gated_fwd_kernel<F32, true><<<grid, block, 0, s>>>(a);
-        else gated_fwd_kernel<F32, false><<<grid, block, 0, s>>>(a);
+// Of any type and alignment these sizes may come in.
+int64_t gated_fwd_scratch(int64_t Bt, int64_t Dn, int64_t L) {
+    int64_t n = 0;
+    for (int k = 0; k < 4 && Bt * Dn > 0; ++k) {
+        const Plan p = plan_of(Bt * Dn, L, k & 1, k & 2);
+        n = std::max(n, p.S > 1 ? 2 * Bt * Dn * p.S : 0);
     }
-    return hipGetLastError();
+    return n;
+}
+int64_t gated_bwd_scratch(int64_t Bt, int64_t Dn, int64_t L) {
+    int64_t n = 0;
+    for (int k = 0; k < 4 && Bt * Dn > 0; ++k) {
+        const Plan p = plan_of(Bt * Dn, L, k & 1, k & 2);
+        n = std::max(n, Bt * Dn * ((p.S > 1 ? 2 * p.S : 0) + (p.parts(Bt) ? p.S : 0)));
+    }
+    return n;
 }
 
-hipError_t launch_gated_bwd(const GatedLaunch& l, hipStream_t s) {
-    const GArgs a = args_of(l);
-    const dim3 grid(blocks_for(a.R, 4)), block(256);
-    if (l.bf16) {
-        if (l.vec_ok) gated_bwd_kernel<BF16, true><<<grid, block, 0, s>>>(a);
-        else gated_bwd_kernel<BF16, false><<<grid, block, 0, s>>>(a);
-    } else {
-        if (l.vec_ok) gated_bwd_kernel<F32, true><<<grid, block, 0, s>>>(a);
-        else gated_bwd_kernel<F32, false><<<grid, block, 0, s>>>(a);
-    }
-    gated_rate_kernel<<<dim3(blocks_for(a.Dn, 256)), block, 0, s>>>(a.drate_part, l.drate, a.Dn, l.Bt);
-    return hipGetLastError();
-}
+hipError_t launch_gated_fwd(const GatedLaunch& l, hipStream_t s) { return run(l, false, s); }
+hipError_t launch_gated_bwd(const GatedLaunch& l, hipStream_t s) { return run(l, true, s); }
 
 hipError_t launch_gated_update(const GatedUpdateLaunch& l, hipStream_t s) {
     const dim3 grid(blocks_for(l.R, 256)), block(256);

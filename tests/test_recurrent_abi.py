@@ -191,9 +191,10 @@ def test_conv_wide_kernel_is_unsupported():
 
 
 def test_scratch_queries():
-    assert mss.gated_scan_scratch(4, 5120, 2048)[1] >= 4 * 5120
-    assert mss.causal_conv1d_bwd_scratch(4, 5120, 2048, 4) >= 5 * 4 * 5120
-    assert mss.beam_select_scratch(1, 1, 1, 1) >= 5
+    for shape in ((4, 5120, 2048), (1, 64, 131072), (2, 3, 0), (0, 5, 9), (3, 0, 4)):
+        assert all(0 <= n < 1 << 40 for n in mss.gated_scan_scratch(*shape))
+        assert 0 <= mss.causal_conv1d_bwd_scratch(*shape, 4) < 1 << 40
+    assert mss.beam_select_scratch(1, 1, 1, 1) >= 5  # a maximum, a sum of 64 bits, a logit, a token
     for f, args in ((mss.gated_scan_scratch, (-1, 4, 4)), (mss.gated_scan_scratch, (1 << 40, 1 << 40, 4)),
                     (mss.causal_conv1d_bwd_scratch, (2, 4, 4, 0)), (mss.beam_select_scratch, (1, 0, 5, 1))):
         with pytest.raises(mss.MssError) as e:
