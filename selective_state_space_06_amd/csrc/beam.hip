@@ -4,22 +4,26 @@
 // Selection.  A live beam's continuation by token v scores score + logit_v - log sum exp(logits);
 // a finished beam has one, its end token at its own score.  Per request the k best are kept.  A
 // beam's continuations are ordered by their logits alone, so one pass over the logits gives both a
-// slice's running maximum and sum of exponentials and its k best (slices kernel); a second, small
-// kernel joins the slices of a beam, forms the scores and joins the beams.  Scores are compared in
-// 64 bits: they differ by the beams' sums and normalisers, whose 32-bit rounding would decide
-// between near candidates.
+// slice's greatest logit and sum of exponentials and its k best (slices kernel); a second, small
+// kernel forms the slices' scores and merges a request's lists.  Scores are compared in 64 bits: they
+// differ by the beams' sums and normalisers, whose 32-bit rounding would decide between near
+// candidates.
 //
-// The k best are a list spread over a wave, entry j in lane j, best first (a higher value, then a
-// lower position).  A candidate that beats entry k - 1 is inserted by a shift of the entries behind
-// it.  After the first tile few candidates do, and a tile without one costs a compare.
+// Logits are compared as whole numbers of the same order (order_of), with the token behind them as one
+// 64-bit key (a higher value, then a lower token).  A wave keeps its k best as a list spread over its
+// lanes, entry j in lane j, best first; a candidate that beats entry k - 1 is inserted by a shift of the
+// entries behind it.  Of n values in no order about k (1 + ln(n / k)) do so when they come, and a tile
+// without one costs a compare; the first tile is cut at (16 bits of) the k-th greatest of its lanes'
+// greatest values first, which leaves little more than k of it.  Sorted lists are merged by taking the
+// greatest head k times.
+#include <algorithm>
+
 #include "device_math.hpp"
 #include "mss_internal.hpp"
+#include "row_io.hpp"
 
 namespace mss {
 namespace {
-
-constexpr int kE = 8;
-constexpr int kTile = 64 * kE;
 
 struct SArgs {
     const void* logits;      // (Bt, N, V)
@@ -29,241 +33,305 @@ struct SArgs {
     int32_t* parents;
     int32_t* tokens;
     int32_t* next_finished;  // nullable
-    double* part_s;          // (rows, splits): sum of exp(logit - part_m)
-    float* part_m;           // (rows, splits): greatest logit, -inf when there is none
-    float* cand_v;           // (rows, splits, K): logits, best first; -inf: no entry
-    int32_t* cand_i;         // (rows, splits, K): tokens
-    int64_t Bt, V, slice;
-    int N, K, splits, end;   // end: -1 for none
+    double* part_s;          // (rows, slices): sum of e^(logit - part_m)
+    float* part_m;           // (rows, slices): greatest logit, -inf when there is none
+    uint64_t* cand;          // (rows, slices, K): keys, best first; kNone: no entry
+    int64_t Bt, V;
+    int64_t tiles;           // per slice
+    int N, K, slices, end;   // end: -1 for none
 };
 
-__device__ __forceinline__ float lane_of(float v, int lane) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
-}
-__device__ __forceinline__ int lane_of(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
-__device__ __forceinline__ uint64_t join64(uint32_t hi, uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; }
-__device__ __forceinline__ uint64_t lane_of(uint64_t v, int lane) {
-    return join64(__builtin_amdgcn_readlane(static_cast<int>(v >> 32), lane),
-                  __builtin_amdgcn_readlane(static_cast<int>(v), lane));
-}
+using mss::lane_of;
 __device__ __forceinline__ int shift_up(int v) { return __builtin_amdgcn_update_dpp(v, v, 0x138, 0xF, 0xF, false); }
-__device__ __forceinline__ float shift_up(float v) { return __int_as_float(shift_up(__float_as_int(v))); }
-__device__ __forceinline__ uint64_t shift_up(uint64_t v) {
-    return join64(shift_up(static_cast<int>(v >> 32)), shift_up(static_cast<int>(v)));
+__device__ __forceinline__ uint64_t join64(uint32_t hi, uint32_t lo) { return static_cast<uint64_t>(hi) << 32 | lo; }
+
+__device__ __forceinline__ uint64_t ballot(bool b) { return __builtin_amdgcn_ballot_w64(b); }
+__device__ __forceinline__ int first_of(uint64_t lanes) { return __builtin_ctzll(lanes); }
+__device__ __forceinline__ uint32_t lane_of(uint32_t v, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), lane));
+}
+__device__ __forceinline__ uint64_t lane_of(uint64_t v, int lane) {
+    return join64(lane_of(static_cast<uint32_t>(v >> 32), lane), lane_of(static_cast<uint32_t>(v), lane));
+}
+// The greatest of every lane's w, the same in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t w) {
+#define MSS_MAX(CTRL, ROWS)                                                                                      \
+    {                                                                                                            \
+        const uint32_t o = __builtin_amdgcn_update_dpp(0, static_cast<int>(w), CTRL, ROWS, 0xF, false);          \
+        w = o > w ? o : w;                                                                                       \
+    }
+    MSS_MAX(0x111, 0xF)  // the steps of wave_sum
+    MSS_MAX(0x112, 0xF)
+    MSS_MAX(0x114, 0xF)
+    MSS_MAX(0x118, 0xF)
+    MSS_MAX(0x142, 0xA)
+    MSS_MAX(0x143, 0xC)
+#undef MSS_MAX
+    return lane_of(w, 63);
 }
 
-// A 64-bit score as a whole number of the same order, 0 for a score that is -inf or not a number (a
-// list's empty entry).  The second list holds these, and no double: the compiler here encodes a scalar
-// move of a 64-bit -inf as one of 0 (the literal's low half).  For the same reason -inf is told by its
-// two halves.
-__device__ __forceinline__ uint64_t key_of(double s) {
-    s += 0.0;  // -0 orders as +0
+// Floats as whole numbers of the same order (-0 as +0), and back.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const int b = __float_as_int(v + 0.0f);
+    return static_cast<uint32_t>(b ^ (b >> 31 | INT32_MIN));
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    const int b = static_cast<int>(o);
+    return __int_as_float(b ^ (~(b >> 31) | INT32_MIN));
+}
+constexpr uint32_t kLeast = 0x00800000u;  // order_of the least finite value; -inf is one less
+// A logit and its token.  kNone comes before every key of a finite or +inf logit and after those of -inf.
+__device__ __forceinline__ uint64_t key_of(uint32_t order, int token) { return join64(order, ~static_cast<uint32_t>(token)); }
+__device__ __forceinline__ int token_of(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
+constexpr uint64_t kNone = static_cast<uint64_t>(kLeast) << 32;
+
+// A 64-bit score in the same way, 0 for a score that is -inf or not a number.  The merge compares these and
+// no doubles: the compiler here encodes a scalar move of a 64-bit -inf as one of 0 (the literal's low
+// half).  For the same reason -inf is told by its two halves.
+__device__ __forceinline__ uint64_t order64_of(double s) {
+    s += 0.0;
     const uint32_t hi = __double2hiint(s), lo = __double2loint(s);
     if (s != s || (hi == 0xFFF00000u && lo == 0u)) return 0;
     const uint32_t flip = static_cast<uint32_t>(static_cast<int32_t>(hi) >> 31);
     return join64(hi ^ (flip | 0x80000000u), lo ^ flip);
 }
-__device__ __forceinline__ float score_of(uint64_t key) {  // of a key that is not 0
-    const uint32_t hi = static_cast<uint32_t>(key >> 32), lo = static_cast<uint32_t>(key);
+__device__ __forceinline__ float score_of(uint64_t order) {  // of one that is not 0
+    const uint32_t hi = static_cast<uint32_t>(order >> 32), lo = static_cast<uint32_t>(order);
     const uint32_t flip = static_cast<uint32_t>(~(static_cast<int32_t>(hi) >> 31));
     return static_cast<float>(__hiloint2double(static_cast<int>(hi ^ (flip | 0x80000000u)), static_cast<int>(lo ^ flip)));
 }
 
-template <class T> __device__ __forceinline__ T none();
-template <> __device__ __forceinline__ float none<float>() { return -INFINITY; }
-template <> __device__ __forceinline__ uint64_t none<uint64_t>() { return 0; }
-
-// The list of a wave: lane j holds the j-th best, none / INT_MAX where there is none yet.
-template <class T>
+// The list of a wave: lane j holds the j-th best key.
 struct List {
-    T v;
-    int i;
-    T last_v;  // entry k - 1, the same in every lane
-    int last_i;
-    __device__ __forceinline__ void clear() {
-        v = last_v = none<T>();
-        i = last_i = INT32_MAX;
-    }
-    // true where (w, j) would enter; never for none or a value that is not a number
-    __device__ __forceinline__ bool takes(T w, int j) const {
-        return w > last_v || (w == last_v && j < last_i && w > none<T>());
-    }
-    // w and j the same in every lane
-    __device__ __forceinline__ void insert(T w, int j, int k, int lane) {
-        const bool ahead = v > w || (v == w && i < j);
-        const int at = __popcll(__ballot(ahead));
-        const T sv = shift_up(v);
-        const int si = shift_up(i);
-        if (lane > at) v = sv, i = si;
-        else if (lane == at) v = w, i = j;
-        last_v = lane_of(v, k - 1);
-        last_i = lane_of(i, k - 1);
-    }
-    // every lane's (w, j) offered, in any order; w = none for a lane without one
-    __device__ __forceinline__ void offer(T w, int j, int k, int lane) {
-        uint64_t left = __ballot(takes(w, j));
-        while (left) {
-            const int src = __ffsll(static_cast<unsigned long long>(left)) - 1;
-            insert(lane_of(w, src), lane_of(j, src), k, lane);
-            if (lane == src) w = none<T>();
-            left = __ballot(takes(w, j));
-        }
+    uint64_t key = kNone;
+    uint64_t last = kNone;  // entry k - 1, the same in every lane
+    // the same new key in every lane
+    __device__ __forceinline__ void insert(uint64_t n, int k, int lane) {
+        const int at = __popcll(ballot(key > n));
+        const uint64_t below = join64(shift_up(static_cast<int>(key >> 32)), shift_up(static_cast<int>(key)));
+        key = lane > at ? below : lane == at ? n : key;
+        last = lane_of(key, k - 1);
     }
 };
 
-// One wave per (row, slice of the vocabulary).  VEC: rows are whole aligned 16-byte vectors.
+// The k greatest of `count` (at most 64) sorted lists of k keys, one behind the other, in lane order.
+__device__ __forceinline__ uint64_t merge_lists(const uint64_t* lists, int count, int k, int lane) {
+    uint64_t mine = kNone, head = lane < count ? lists[lane * k] : kNone;
+    int at = 0;
+    for (int j = 0; j < k; ++j) {
+        const uint32_t most = wave_max(static_cast<uint32_t>(head >> 32));
+        if (most <= kLeast && ballot(head > kNone) == 0) break;
+        uint64_t who = ballot(static_cast<uint32_t>(head >> 32) == most);
+        if (who & (who - 1)) {  // equal logits: the lowest token
+            const uint32_t low = wave_max(static_cast<uint32_t>(head >> 32) == most ? static_cast<uint32_t>(head) : 0);
+            who = ballot(head == join64(most, low));
+        }
+        const int src = first_of(who);
+        const uint64_t key = lane_of(head, src);
+        if (lane == j) mine = key;
+        if (lane == src) head = ++at < k ? lists[lane * k + at] : kNone;
+    }
+    return mine;
+}
+
+// One block per (row, slice of the vocabulary), its waves on successive parts of the slice, each with two
+// tiles on their way (64 x 8 x 128008 f32: 47 us, the card's read rate; one wave with one tile on its way and
+// a list of values and tokens apart 57).  VEC: rows are whole aligned 16-byte vectors.
+constexpr int kWaves = 8;
+
 template <class E, bool VEC>
-__global__ __launch_bounds__(256) void beam_slices_kernel(SArgs a) {
-    constexpr int V = E::kPerVec;
+__global__ __launch_bounds__(64 * kWaves) void beam_slices_kernel(SArgs a) {
+    using S = typename E::storage;
+    __shared__ uint64_t all[kWaves * kBeamMost];
+    __shared__ double all_s[kWaves];
+    __shared__ float all_m[kWaves];
     const int lane = threadIdx.x & 63;
-    const int64_t works = a.Bt * a.N * a.splits;
-    for (int64_t g = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); g < works; g += (int64_t)gridDim.x * 4) {
-        const int64_t row = g / a.splits, split = g % a.splits;
-        const int64_t lo = split * a.slice, hi = lo + a.slice < a.V ? lo + a.slice : a.V;
-        const auto* p = static_cast<const typename E::storage*>(a.logits) + row * a.V;
-        List<float> list;
-        list.clear();
-        float m = -INFINITY, s = 0.0f;  // of this lane's elements
-        // a beam at its end or without a score has no continuation that needs its logits
-        const float score = a.scores[row];
-        const bool skip = (a.finished && a.finished[row] != 0) || !(score > -INFINITY);
-        for (int64_t t = lo; !skip && t < hi; t += kTile) {
-            const int64_t t0 = t + lane * kE;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    const int64_t works = a.Bt * a.N * a.slices, tiles = (a.V + kTile - 1) / kTile;
+    for (int64_t g = blockIdx.x; g < works; g += gridDim.x) {
+        const int64_t row = g / a.slices, from = g % a.slices * a.tiles;
+        const int64_t to = from + a.tiles < tiles ? from + a.tiles : tiles;
+        const int64_t per = (to - from + kWaves - 1) / kWaves;
+        const int64_t lo = from + wave * per, hi = lo + per < to ? lo + per : to;  // this wave's tiles
+        const S* p = static_cast<const S*>(a.logits) + row * a.V;
+        List list;
+        float m = -INFINITY, s = 0.0f;  // of this lane's elements: the greatest, the sum of e^(v - m)
+        Raw<E> raw[2] = {};
+        const auto load = [&](int64_t k, Raw<E>& r) {
+            load8<E, VEC>(p + k * kTile, a.V, clamp_tile(a.V - k * kTile), lane, r);
+        };
+        const auto tile = [&](int64_t k, Raw<E>& r, auto first) {
+            const int rem = clamp_tile(a.V - k * kTile);
+            settle8<E, VEC>(a.V, rem, lane, r);
             float v[kE];
+            r.unpack(v);
+            if (k + 2 < hi) load(k + 2, r);
+            if (rem < kTile) {
 #pragma unroll
-            for (int j = 0; j < kE / V; ++j) {
-                const int64_t q = t0 + j * V;
-                if (q + V <= hi) {
-                    uint4 w;
-                    if (VEC) w = *reinterpret_cast<const uint4*>(p + q);
-                    else __builtin_memcpy(&w, p + q, 16);
-                    E::unpack(w, v + j * V);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < V; ++e) v[j * V + e] = q + e < hi ? E::load1(p, q + e) : -INFINITY;
-                }
+                for (int e = 0; e < kE; ++e)
+                    if (lane * kE + e >= rem) v[e] = -INFINITY;
             }
-            float best = -INFINITY;
+            const auto sums = [&]() {
+                float best = v[0];
+#pragma unroll
+                for (int e = 1; e < kE; ++e) best = fmaxf(best, v[e]);
+                const float up = fmaxf(m, best), ref = up > -INFINITY ? up : 0.0f;
+                float t = 0.0f;
+#pragma unroll
+                for (int e = 0; e < kE; ++e) t += fast_exp2((v[e] - ref) * kLog2e);
+                return make_float3(best, up, t);
+            };
+            float3 b = sums();
+            if (b.z != b.z) {  // a NaN logit, which is masked (or one of +inf)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) v[e] = v[e] == v[e] ? v[e] : -INFINITY;
+                b = sums();
+            }
+            if (b.y > m) {
+                s *= fast_exp2((m - b.y) * kLog2e);
+                m = b.y;
+            }
+            s += b.z;
+            const uint32_t most = order_of(b.x);
+            uint32_t bar = static_cast<uint32_t>(list.last >> 32);  // nothing below it is among the k best
+            if (decltype(first)::value) {
+                uint32_t cut = 0;
+#pragma unroll
+                for (int bit = 31; bit >= 16; --bit) {
+                    const uint32_t t = cut | 1u << bit;
+                    if (__popcll(ballot(most >= t)) >= a.K) cut = t;
+                }
+                bar = cut > bar ? cut : bar;
+            }
+            if (ballot(most >= bar) == 0) return;
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
-                v[e] = v[e] == v[e] ? v[e] : -INFINITY;  // a NaN logit is masked
-                best = fmaxf(best, v[e]);
+                const uint32_t o = order_of(v[e]);
+                const uint64_t key = key_of(o, static_cast<int>(k * kTile) + lane * kE + e);
+                uint64_t left = ballot((o >= bar) & (key > list.last));
+                while (left) {
+                    list.insert(lane_of(key, first_of(left)), a.K, lane);
+                    left &= left - 1;
+                    left &= ballot(key > list.last);
+                }
             }
-            if (best > m) {
-                s *= fast_exp2((m - best) * kLog2e);
-                m = best;
+        };
+        // a beam at its end or without a score has no continuation that needs its logits
+        const float score = a.scores[row];
+        if (lo < hi && !(a.finished && a.finished[row] != 0) && score > -INFINITY) {
+            load(lo, raw[0]);
+            if (lo + 1 < hi) load(lo + 1, raw[1]);
+            tile(lo, raw[0], True{});
+            for (int64_t k = lo + 1; k < hi; k += 2) {
+                tile(k, raw[1], False{});
+                if (k + 1 < hi) tile(k + 1, raw[0], False{});
             }
-            const float ref = m > -INFINITY ? m : 0.0f;
+        }
+        // the lanes' sums joined in 64 bits
+        const float top = value_of(wave_max(order_of(m)));
+        double sum = m > -INFINITY ? static_cast<double>(s) * fast_exp2((m - top) * kLog2e) : 0.0;
 #pragma unroll
-            for (int e = 0; e < kE; ++e) s += fast_exp2((v[e] - ref) * kLog2e);
-            // the lanes' best that enter the list, one at a time
-            int bi = 0;
-            for (;;) {
+        for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
+        if (lane == 0) {
+            all_m[wave] = top;
+            all_s[wave] = sum;
+        }
+        if (lane < a.K) all[wave * a.K + lane] = list.key;
+        __syncthreads();
+        if (wave == 0) {
+            const float wm = lane < kWaves ? all_m[lane] : -INFINITY, most = value_of(wave_max(order_of(wm)));
+            double ws = wm > -INFINITY ? all_s[lane] * fast_exp2((wm - most) * kLog2e) : 0.0;
 #pragma unroll
-                for (int e = kE - 1; e >= 0; --e) bi = v[e] == best ? e : bi;
-                const int at = static_cast<int>(t0) + bi;
-                const uint64_t left = __ballot(list.takes(best, at));
-                if (!left) break;
-                const int src = __ffsll(static_cast<unsigned long long>(left)) - 1;
-                list.insert(lane_of(best, src), lane_of(at, src), a.K, lane);
-                if (lane == src) {
-                    best = -INFINITY;
+            for (int x = kWaves / 2; x > 0; x >>= 1) ws += __shfl_xor(ws, x);
+            if (lane == 0) {
+                a.part_m[g] = most;
+                a.part_s[g] = ws;
+            }
+            const uint64_t got = merge_lists(all, kWaves, a.K, lane);
+            if (lane < a.K) a.cand[g * a.K + lane] = got;
+        }
+        __syncthreads();
+    }
+}
+
+// One block per request: its waves merge the slices' lists of the beams in turn, then the first wave the
+// beams' lists, a lane to each.  Shared memory: the lists.
+constexpr int kMergeWaves = 8;
+__global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(SArgs a) {
+    extern __shared__ uint64_t lists[];  // (N, slices, K); a beam's merged list ends up in its first
+    __shared__ double scores[kBeamMost], norms[kBeamMost];
+    __shared__ int done[kBeamMost];
+    const int each = a.slices * a.K;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
+    for (int64_t b = blockIdx.x; b < a.Bt; b += gridDim.x) {
+        for (int e = threadIdx.x; e < a.N * each; e += 64 * kMergeWaves) lists[e] = a.cand[b * a.N * each + e];
+        __syncthreads();
+        for (int n = wave; n < a.N; n += kMergeWaves) {
+            const int64_t row = b * a.N + n;
+            const float m = lane < a.slices ? a.part_m[row * a.slices + lane] : -INFINITY;
+            double sum = lane < a.slices ? a.part_s[row * a.slices + lane] : 0.0;
+            const float top = value_of(wave_max(order_of(m)));
+            if (a.slices > 1) {
+                sum = m > -INFINITY ? sum * exp(static_cast<double>(m) - top) : 0.0;
 #pragma unroll
-                    for (int e = 0; e < kE; ++e) {
-                        if (e == bi) v[e] = -INFINITY;
-                        best = fmaxf(best, v[e]);
+                for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
+                const uint64_t got = merge_lists(lists + n * each, a.slices, a.K, lane);
+                if (lane < a.K) lists[n * each + lane] = got;
+            }
+            if (lane == 0) {
+                scores[n] = a.scores[row];
+                norms[n] = static_cast<double>(top) + log(sum);
+                done[n] = a.finished && a.finished[row] != 0;
+            }
+        }
+        __syncthreads();
+        if (wave == 0) {
+            // lane n: beam n's next continuation, its score as a whole number (0: none left)
+            const int n = lane < a.N ? lane : 0;
+            const bool over = done[n];
+            int at = 0, token = 0;
+            uint64_t order = 0;
+            const auto next = [&]() {
+                order = 0;
+                if (over) {  // one continuation
+                    if (at == 0) order = order64_of(scores[n]);
+                    token = a.end;
+                } else if (at < a.K) {
+                    const uint64_t key = lists[n * each + at];
+                    if (key > kNone)
+                        order = order64_of(scores[n] + (static_cast<double>(value_of(key >> 32)) - norms[n]));
+                    token = token_of(key);
+                }
+            };
+            if (lane < a.N) next();
+            for (int j = 0; j < a.K; ++j) {
+                const uint32_t hi = static_cast<uint32_t>(order >> 32), lo = static_cast<uint32_t>(order);
+                const uint32_t most = wave_max(hi);
+                uint64_t who = ballot(hi == most);
+                if (who & (who - 1)) {
+                    const uint32_t low = wave_max(hi == most ? lo : 0);
+                    who = ballot((hi == most) & (lo == low));
+                }
+                if (lane == first_of(who)) {  // of equal scores the earlier beam's
+                    const bool some = order != 0;
+                    const int64_t o = b * a.K + j;
+                    a.next_scores[o] = some ? score_of(order) : -INFINITY;
+                    a.parents[o] = some ? n : 0;
+                    a.tokens[o] = some ? token : 0;
+                    if (a.next_finished) a.next_finished[o] = some && (over || token == a.end);
+                    if (some) {
+                        ++at;
+                        next();
                     }
                 }
             }
         }
-        // the lanes' maxima and sums joined, the sums in 64 bits
-        float top = m;
-#pragma unroll
-        for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-        double sum = top > -INFINITY ? static_cast<double>(s) * fast_exp2((m - top) * kLog2e) : 0.0;
-#pragma unroll
-        for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
-        if (lane == 0) {
-            a.part_m[g] = top;
-            a.part_s[g] = sum;
-        }
-        if (lane < a.K) {
-            a.cand_v[g * a.K + lane] = list.v;
-            a.cand_i[g * a.K + lane] = list.i;
-        }
-    }
-}
-
-// One block per request: its waves join the slices of the beams in turn, then the first wave joins
-// the beams.  Shared memory: N K scores (as keys), N K tokens, N flags.
-__global__ __launch_bounds__(256) void beam_join_kernel(SArgs a) {
-    extern __shared__ uint64_t shared[];
-    uint64_t* sc = shared;
-    int* tok = reinterpret_cast<int*>(sc + a.N * a.K);
-    int* fin = tok + a.N * a.K;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t b = blockIdx.x; b < a.Bt; b += gridDim.x) {
-        for (int n = wave; n < a.N; n += 4) {
-            const int64_t row = b * a.N + n;
-            const double score = a.scores[row];
-            const bool done = a.finished && a.finished[row] != 0;
-            uint64_t total = 0;
-            int token = 0;
-            if (done) {
-                if (lane == 0) total = key_of(score), token = a.end;
-            } else {
-                List<float> list;
-                list.clear();
-                const int64_t first = row * a.splits;
-                const float m = lane < a.splits ? a.part_m[first + lane] : -INFINITY;
-                float top = m;
-#pragma unroll
-                for (int x = 32; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-                double sum = 0.0;
-                if (lane < a.splits && m > -INFINITY) sum = a.part_s[first + lane] * exp(static_cast<double>(m) - top);
-#pragma unroll
-                for (int x = 32; x > 0; x >>= 1) sum += __shfl_xor(sum, x);
-                const double lse = static_cast<double>(top) + log(sum);
-                const int all = a.splits * a.K;
-                for (int c = 0; c < all; c += 64) {
-                    const bool ok = c + lane < all;
-                    list.offer(ok ? a.cand_v[first * a.K + c + lane] : -INFINITY,
-                               ok ? a.cand_i[first * a.K + c + lane] : 0, a.K, lane);
-                }
-                if (list.v > -INFINITY) {
-                    total = key_of(score + (static_cast<double>(list.v) - lse));
-                    token = list.i;
-                }
-            }
-            if (lane < a.K) {
-                sc[n * a.K + lane] = total;
-                tok[n * a.K + lane] = token;
-            }
-            if (lane == 0) fin[n] = done;
-        }
-        __syncthreads();
-        if (wave == 0) {
-            List<uint64_t> list;
-            list.clear();
-            const int all = a.N * a.K;
-            for (int c = 0; c < all; c += 64)
-                list.offer(c + lane < all ? sc[c + lane] : 0, c + lane, a.K, lane);
-            if (lane < a.K) {
-                const bool some = list.v != 0;
-                const int at = some ? list.i : 0;
-                const int parent = some ? at / a.K : 0, token = some ? tok[at] : 0;
-                const int64_t o = b * a.K + lane;
-                a.next_scores[o] = some ? score_of(list.v) : -INFINITY;
-                a.parents[o] = parent;
-                a.tokens[o] = token;
-                if (a.next_finished) a.next_finished[o] = some && (fin[parent] || token == a.end);
-            }
-        }
         __syncthreads();
     }
 }
 
-// ---- reordering.  Thread per (tensor, request, 16-, 4- or 2-byte unit of a beam's state): every
+// ---- reordering.  Thread per (tensor, request, 16-, 8-, 4- or 2-byte unit of a beam's state): every
 // beam's unit is read before any is written, so the states move in place; a beam that is its own
 // parent is neither read for itself nor written.
 struct RArgs {
@@ -275,65 +343,79 @@ struct RArgs {
     int count, N;
 };
 
-template <class U, int MOST>
+// NU units a thread, 256 apart.
+template <class U, int MOST, int NU>
 __global__ __launch_bounds__(256) void beam_reorder_kernel(RArgs a) {
     for (int64_t blk = blockIdx.x; blk < a.first[a.count]; blk += gridDim.x) {
         int t = 0;
         while (blk >= a.first[t + 1]) ++t;
-        const int64_t units = a.units[t], per = (units + 255) / 256;
+        const int64_t units = a.units[t], per = (units + 256 * NU - 1) / (256 * NU);
         const int64_t b = (blk - a.first[t]) / per;
-        const int64_t u = (blk - a.first[t]) % per * 256 + threadIdx.x;
-        if (u >= units) continue;
+        const int64_t u = (blk - a.first[t]) % per * (256 * NU) + threadIdx.x;
         U* base = reinterpret_cast<U*>(a.data[t]) + b * a.N * units + u;
         const int32_t* par = a.parents + b * a.N;
-        U v[MOST];
+        U v[MOST][NU];
 #pragma unroll
         for (int j = 0; j < MOST; ++j) {
-            if (j < a.N) {
-                const int p = par[j];
-                if (p != j && p >= 0 && p < a.N) v[j] = base[p * units];
+            const int p = j < a.N ? par[j] : j;
+            if (p != j && p >= 0 && p < a.N) {
+#pragma unroll
+                for (int k = 0; k < NU; ++k)
+                    if (u + 256 * k < units) v[j][k] = base[p * units + 256 * k];
             }
         }
 #pragma unroll
         for (int j = 0; j < MOST; ++j) {
-            if (j < a.N) {
-                const int p = par[j];
-                if (p != j && p >= 0 && p < a.N) base[j * units] = v[j];
+            const int p = j < a.N ? par[j] : j;
+            if (p != j && p >= 0 && p < a.N) {
+#pragma unroll
+                for (int k = 0; k < NU; ++k)
+                    if (u + 256 * k < units) base[j * units + 256 * k] = v[j][k];
             }
         }
     }
 }
 
-template <class U>
-void reorder_u(const RArgs& a, hipStream_t s) {
+// A 16-byte unit as a native vector: an array of HIP's struct would not stay in registers.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <class U, int MOST, int NU>
+void reorder_n(RArgs& a, hipStream_t s) {
+    for (int t = 0; t < a.count; ++t) a.first[t + 1] = a.first[t] + a.Bt * ((a.units[t] + 256 * NU - 1) / (256 * NU));
     const int64_t total = a.first[a.count];
-    const dim3 grid(static_cast<unsigned>(total < (1 << 22) ? total : (1 << 22))), block(256);
-    if (a.N <= 4) beam_reorder_kernel<U, 4><<<grid, block, 0, s>>>(a);
-    else if (a.N <= 8) beam_reorder_kernel<U, 8><<<grid, block, 0, s>>>(a);
-    else if (a.N <= 16) beam_reorder_kernel<U, 16><<<grid, block, 0, s>>>(a);
-    else beam_reorder_kernel<U, 64><<<grid, block, 0, s>>>(a);
+    const dim3 grid(static_cast<unsigned>(total < (1 << 22) ? total : (1 << 22)));
+    beam_reorder_kernel<U, MOST, NU><<<grid, dim3(256), 0, s>>>(a);
+}
+template <class U>
+void reorder_u(RArgs& a, hipStream_t s) {
+    if (a.N <= 4) reorder_n<U, 4, 2>(a, s);
+    else if (a.N <= 8) reorder_n<U, 8, 1>(a, s);
+    else if (a.N <= 16) reorder_n<U, 16, 1>(a, s);
+    else if (sizeof(U) == 16 || a.N <= 32) reorder_n<U, 32, 1>(a, s);
+    else if constexpr (sizeof(U) < 16) reorder_n<U, 64, 1>(a, s);
 }
 
-// Slices per row: enough waves to fill the chip, none shorter than a tile, at most one per lane of
-// the joining wave.
-void plan_select(int64_t rows, int64_t V, int64_t* slice, int* splits) {
-    int64_t n = (4096 + rows - 1) / (rows < 1 ? 1 : rows);
+// Slices per row: blocks for every CU twice over, each wave with a tile, and lists that fit the merging
+// block's shared memory.
+constexpr int64_t kMergeBytes = 56 << 10;
+void plan_select(int64_t rows, int64_t N, int64_t V, int64_t K, int64_t* per, int* slices) {
     const int64_t tiles = (V + kTile - 1) / kTile;
-    if (n > 64) n = 64;
-    if (n > tiles) n = tiles;
-    if (n < 1) n = 1;
-    const int64_t per = (tiles + n - 1) / n;
-    *slice = (per < 1 ? 1 : per) * kTile;
-    *splits = static_cast<int>(tiles > 0 ? (V + *slice - 1) / *slice : 1);
+    int64_t n = (512 + rows - 1) / rows;
+    n = std::min(n, (tiles + kWaves - 1) / kWaves);
+    n = std::max<int64_t>(1, std::min({n, kMergeBytes / (8 * N * K), int64_t{64}}));  // 32 KB for 64 beams of 64
+    *per = (tiles + n - 1) / n;
+    *slices = static_cast<int>((tiles + *per - 1) / *per);
 }
 
 }  // namespace
 
 int64_t beam_select_scratch(int64_t Bt, int64_t N, int64_t V, int64_t K) {
-    int64_t slice;
-    int splits;
-    plan_select(Bt * N, V, &slice, &splits);
-    return Bt * N * splits * (3 + 2 * K);
+    if (Bt == 0) return 0;
+    int64_t per;
+    int slices;
+    plan_select(Bt * N, N, V, K, &per, &slices);
+    return Bt * N * slices * (3 + 2 * K);
 }
 
 hipError_t launch_beam_select(const BeamSelectLaunch& l, hipStream_t s) {
@@ -341,14 +423,12 @@ hipError_t launch_beam_select(const BeamSelectLaunch& l, hipStream_t s) {
     a.logits = l.logits; a.scores = l.scores; a.finished = l.finished; a.next_scores = l.next_scores;
     a.parents = l.parents; a.tokens = l.tokens; a.next_finished = l.next_finished;
     a.Bt = l.Bt; a.V = l.V; a.N = static_cast<int>(l.N); a.K = static_cast<int>(l.K); a.end = l.end;
-    plan_select(l.Bt * l.N, l.V, &a.slice, &a.splits);
-    const int64_t works = l.Bt * l.N * a.splits;
+    plan_select(l.Bt * l.N, l.N, l.V, l.K, &a.tiles, &a.slices);
+    const int64_t works = l.Bt * l.N * a.slices;
     a.part_s = reinterpret_cast<double*>(l.scratch);
-    a.part_m = l.scratch + 2 * works;
-    a.cand_v = a.part_m + works;
-    a.cand_i = reinterpret_cast<int32_t*>(a.cand_v + works * l.K);
-    const int64_t blocks = (works + 3) / 4;
-    const dim3 grid(static_cast<unsigned>(blocks < (1 << 22) ? blocks : (1 << 22))), block(256);
+    a.cand = reinterpret_cast<uint64_t*>(a.part_s + works);
+    a.part_m = reinterpret_cast<float*>(a.cand + works * l.K);
+    const dim3 grid(blocks_for(works, 1)), block(64 * kWaves);
     if (l.bf16) {
         if (l.vec_ok) beam_slices_kernel<BF16, true><<<grid, block, 0, s>>>(a);
         else beam_slices_kernel<BF16, false><<<grid, block, 0, s>>>(a);
@@ -356,23 +436,23 @@ hipError_t launch_beam_select(const BeamSelectLaunch& l, hipStream_t s) {
         if (l.vec_ok) beam_slices_kernel<F32, true><<<grid, block, 0, s>>>(a);
         else beam_slices_kernel<F32, false><<<grid, block, 0, s>>>(a);
     }
-    const size_t lds = static_cast<size_t>(a.N) * a.K * 12 + static_cast<size_t>(a.N) * 4;  // at most 49.5 KB
-    beam_join_kernel<<<dim3(static_cast<unsigned>(l.Bt < (1 << 22) ? l.Bt : (1 << 22))), block, lds, s>>>(a);
+    const size_t lds = static_cast<size_t>(a.N) * a.slices * a.K * 8;
+    beam_merge_kernel<<<dim3(blocks_for(l.Bt, 1)), dim3(64 * kMergeWaves), lds, s>>>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_beam_reorder(const BeamReorderLaunch* l, int count, const int32_t* parents, int64_t Bt, int N,
                                hipStream_t s) {
     // one launch per unit size and kReorderMost tensors
-    for (int unit : {16, 4, 2}) {
-        if (unit == 16 && N > 16) continue;  // 64 16-byte units would not stay in registers
+    for (int unit : {16, 8, 4, 2}) {
         RArgs a{};
         a.parents = parents;
         a.Bt = Bt;
         a.N = N;
-        auto flush = [&]() {
+        const auto flush = [&]() {
             if (a.count == 0) return;
-            if (unit == 16) reorder_u<uint4>(a, s);
+            if (unit == 16) reorder_u<u32x4>(a, s);
+            else if (unit == 8) reorder_u<u32x2>(a, s);
             else if (unit == 4) reorder_u<uint32_t>(a, s);
             else reorder_u<uint16_t>(a, s);
             a.count = 0;
@@ -380,11 +460,11 @@ hipError_t launch_beam_reorder(const BeamReorderLaunch* l, int count, const int3
         for (int t = 0; t < count; ++t) {
             const uintptr_t at = reinterpret_cast<uintptr_t>(l[t].data);
             const auto fits = [&](int64_t u) { return l[t].bytes % u == 0 && at % u == 0; };
-            const int mine = N <= 16 && fits(16) ? 16 : fits(4) ? 4 : 2;
+            // (more than 32 units of 16 bytes would not stay in registers)
+            const int mine = N <= 32 && fits(16) ? 16 : fits(8) ? 8 : fits(4) ? 4 : 2;
             if (mine != unit || l[t].bytes == 0) continue;
             a.data[a.count] = static_cast<char*>(l[t].data);
             a.units[a.count] = l[t].bytes / unit;
-            a.first[a.count + 1] = a.first[a.count] + Bt * ((a.units[a.count] + 255) / 256);
             if (++a.count == kReorderMost) flush();
         }
         flush();

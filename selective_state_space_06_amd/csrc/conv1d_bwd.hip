@@ -77,6 +77,8 @@ __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) later[j] = lane_of(dy, j);
         }
+        // lane j: entry j of the final window's gradient
+        const S fin = K > 1 && a.dfin ? static_cast<const S*>(a.dfin)[row * (K - 1) + (lane < K - 1 ? lane : 0)] : 0;
         Raw<E> nx, nd;
         S nh = 0;  // lane j: input j of the K - 1 before the tile, as it lies in memory (converted here, each load was
                    // waited for: 65 us)
@@ -125,10 +127,12 @@ __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_
                 for (int q = 0; q < K; ++q) o[e] = fmaf(w[q], d[e + K - 1 - q], o[e]);
             }
             if (K > 1 && a.dfin && t + kTile > a.L - (K - 1)) {  // the row's last K - 1 inputs left as its window
+                const int64_t j0 = t + lane * kE - (a.L - (K - 1));
 #pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int64_t j = t + lane * kE + e - (a.L - (K - 1));
-                    if (j >= 0 && j < K - 1) o[e] += E::load1(a.dfin, row * (K - 1) + j);
+                for (int j = 0; j < K - 1; ++j) {
+                    const float g = lane_of(E::value(fin), j);
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) o[e] += j0 + e == j ? g : 0.0f;
                 }
             }
             store8<E, VEC>(static_cast<S*>(a.dx) + base + t, rem, lane, o);

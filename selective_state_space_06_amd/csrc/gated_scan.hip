@@ -66,8 +66,6 @@ struct Row {
 // The least q: keeps 1 / m finite where the gate is closed (r = 0, m = 0; m is then 2^-62, and a normal number,
 // which a reciprocal root takes).
 constexpr float kLeastQ = 0x1p-124f;
-struct True { static constexpr bool value = true; };
-struct False { static constexpr bool value = false; };
 __device__ __forceinline__ Row row_of(float rate) {
     Row w;
     w.rate = rate;

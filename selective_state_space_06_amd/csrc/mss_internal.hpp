@@ -236,7 +236,7 @@ hipError_t launch_conv1d_bwd(const ConvBwdLaunch& a, hipStream_t stream);
 
 // Beam search (beam.hip).
 constexpr int kBeamMost = 64;     // beams, and continuations kept, per request
-constexpr int kReorderMost = 32;  // state tensors per launch
+constexpr int kReorderMost = 64;  // state tensors per launch
 
 struct BeamSelectLaunch {
     const void* logits;           // (Bt, N, V)

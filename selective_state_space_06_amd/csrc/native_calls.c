@@ -4,7 +4,7 @@
  * C stack and the library's function is called with them.  The same through ctypes costs about 1.6 us
  * a tensor in the interpreter, more than the kernels of a one-token step take; here it is five attribute
  * reads, about 0.3 us.  Device memory is not touched and no torch header is needed: a tensor is asked by
- * its public attributes (data_ptr, dtype, shape, stride, get_device).
+ * its public attributes (data_ptr, dtype, shape, is_contiguous, get_device).
  *
  * Every function returns the library's status.  Host tensors and tensors of two devices raise
  * ValueError before the call.
@@ -19,7 +19,7 @@
 
 enum { MOST = 16 };
 
-static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_get_device;
+static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_is_contiguous, *s_get_device;
 static PyObject *dtypes[3]; /* torch.float32, torch.bfloat16, torch.int32, in the order of mss_dtype_t */
 
 static int whole(PyObject* o, int64_t* v) {
@@ -81,8 +81,19 @@ static int describe(PyObject* t, mss_tensor_t* d, int64_t* device) {
     for (int k = 0; k < 3; ++k)
         if (dtype == dtypes[k]) d->dtype = k;
     Py_DECREF(dtype);
-    int32_t n;
     if (four(PyObject_GetAttr(t, s_shape), d->shape, &d->ndim)) return -1;
+    PyObject* dense = PyObject_CallMethodNoArgs(t, s_is_contiguous);
+    if (!dense) return -1;
+    Py_DECREF(dense);
+    if (dense == Py_True && d->ndim <= 4) { /* the usual case, without asking for the strides */
+        int64_t step = 1;
+        for (int k = d->ndim - 1; k >= 0; --k) {
+            d->stride[k] = step;
+            step *= d->shape[k];
+        }
+        return 0;
+    }
+    int32_t n;
     return four(PyObject_CallMethodNoArgs(t, s_stride), d->stride, &n);
 }
 
@@ -179,6 +190,38 @@ done:
     return result;
 }
 
+/* The _scratch queries: whole numbers in, (status, floats ...) out. */
+static int sizes(PyObject* const* args, Py_ssize_t n, int64_t* v, Py_ssize_t want) {
+    if (n != want) {
+        PyErr_Format(PyExc_TypeError, "%zd sizes wanted, got %zd", want, n);
+        return -1;
+    }
+    for (Py_ssize_t k = 0; k < n; ++k)
+        if (whole(args[k], &v[k])) return -1;
+    return 0;
+}
+static PyObject* gated_scan_scratch(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+    (void)self;
+    int64_t v[3], fwd = 0, bwd = 0;
+    if (sizes(args, n, v, 3)) return NULL;
+    const int st = mss_gated_scan_scratch(v[0], v[1], v[2], &fwd, &bwd);
+    return Py_BuildValue("iLL", st, (long long)fwd, (long long)bwd);
+}
+static PyObject* causal_conv1d_bwd_scratch(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+    (void)self;
+    int64_t v[4], floats = 0;
+    if (sizes(args, n, v, 4)) return NULL;
+    const int st = mss_causal_conv1d_bwd_scratch(v[0], v[1], v[2], v[3], &floats);
+    return Py_BuildValue("iL", st, (long long)floats);
+}
+static PyObject* beam_select_scratch(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+    (void)self;
+    int64_t v[4], floats = 0;
+    if (sizes(args, n, v, 4)) return NULL;
+    const int st = mss_beam_select_scratch(v[0], v[1], v[2], v[3], &floats);
+    return Py_BuildValue("iL", st, (long long)floats);
+}
+
 /* set_dtypes(torch.float32, torch.bfloat16, torch.int32) */
 static PyObject* set_dtypes(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     (void)self;
@@ -196,7 +239,8 @@ static PyObject* set_dtypes(PyObject* self, PyObject* const* args, Py_ssize_t n)
 #define METHOD(NAME) {#NAME, (PyCFunction)(void (*)(void))NAME, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(gated_scan_fwd),    METHOD(gated_scan_bwd), METHOD(gated_state_update),
                                 METHOD(causal_conv1d_bwd), METHOD(beam_select),    METHOD(beam_reorder),
-                                METHOD(set_dtypes),        {NULL, NULL, 0, NULL}};
+                                METHOD(gated_scan_scratch), METHOD(causal_conv1d_bwd_scratch),
+                                METHOD(beam_select_scratch), METHOD(set_dtypes), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__native(void) {
@@ -204,7 +248,8 @@ PyMODINIT_FUNC PyInit__native(void) {
     s_dtype = PyUnicode_InternFromString("dtype");
     s_shape = PyUnicode_InternFromString("shape");
     s_stride = PyUnicode_InternFromString("stride");
+    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
     s_get_device = PyUnicode_InternFromString("get_device");
-    if (!s_data_ptr || !s_dtype || !s_shape || !s_stride || !s_get_device) return NULL;
+    if (!s_is_contiguous || !s_data_ptr || !s_dtype || !s_shape || !s_stride || !s_get_device) return NULL;
     return PyModule_Create(&module);
 }

@@ -6,6 +6,10 @@
 
 namespace mss {
 
+// Values as types, for lambdas that are built twice.
+struct True { static constexpr bool value = true; };
+struct False { static constexpr bool value = false; };
+
 constexpr int kE = 8;           // steps per lane
 constexpr int kTile = 64 * kE;  // steps per wave and tile
 
