@@ -31,7 +31,7 @@ struct CArgs {
     void* dst;              // (R, K-1), nullable
     float* dw;              // (Dn, K)
     float* db;              // (Dn), nullable
-    float* part;            // (K + 1, R, S): a segment's dw_0 .. dw_{K-1}, dbias, when S > 1
+    float* part;            // (K + 1, R, S): a segment's dw_0 .. dw_{K-1}, dbias; null: dw and db are written
     int64_t Bt, Dn, L, R, tiles;
     int64_t seg_tiles;      // tiles per segment
     int S;                  // segments per row
@@ -152,7 +152,7 @@ __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_
         for (int q = 0; q < K; ++q) s[q] += wave_sum(dw[q]);
         s[K] += wave_sum(db);
     };
-    if (a.S > 1) {
+    if (a.part) {
         for (int64_t it = (int64_t)blockIdx.x * 4 + wave; it < items; it += (int64_t)gridDim.x * 4) {
             float s[K + 1] = {};
             pass(it / a.S, static_cast<int>(it % a.S), s);
@@ -184,17 +184,19 @@ __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_
     }
 }
 
-// The rows of channel d and their segments summed in order.
+// The parts of channel d's rows and their segments summed: a wave per sum, each lane every 64th part in
+// order, then the lanes.
 template <int K>
 __global__ __launch_bounds__(256) void conv_sums_kernel(const float* part, float* dw, float* db, int64_t Dn, int64_t n,
                                                         int S) {
     const int64_t items = Dn * n * S;
-    for (int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; g < Dn * (K + 1);
-         g += (int64_t)gridDim.x * blockDim.x) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t g = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); g < Dn * (K + 1); g += (int64_t)gridDim.x * 4) {
         const int64_t d = g % Dn, k = g / Dn;
         float s = 0.0f;
-        for (int64_t b = 0; b < n; ++b)
-            for (int j = 0; j < S; ++j) s += part[k * items + (b * Dn + d) * S + j];
+        for (int64_t j = lane; j < n * S; j += 64) s += part[k * items + (j / S * Dn + d) * S + j % S];
+        s = wave_sum(s);
+        if (lane != 0) continue;
         if (k < K) dw[d * K + k] = s;
         else if (db) db[d] = s;
     }
@@ -204,6 +206,9 @@ __global__ __launch_bounds__(256) void conv_sums_kernel(const float* part, float
 struct Plan {
     int S;
     int64_t tiles, seg_tiles;
+    bool parts(int64_t Bt, int64_t Dn) const {
+        return S > 1 || goes_by_parts(Bt, Dn, channel_ways(Bt), channel_ways(Bt));
+    }
 };
 Plan plan_of(int64_t R, int64_t L) {
     Plan p;
@@ -216,7 +221,7 @@ Plan plan_of(int64_t R, int64_t L) {
 
 template <class E, int K, bool SILU>
 void launch_v(const CArgs& a, bool vec, hipStream_t s) {
-    const dim3 grid(a.S > 1 ? blocks_for(a.R * a.S, 4) : blocks_for(a.Dn, 4 / channel_ways(a.Bt))), block(256);
+    const dim3 grid(a.part ? blocks_for(a.R * a.S, 4) : blocks_for(a.Dn, 4 / channel_ways(a.Bt))), block(256);
     if (vec) conv_bwd_kernel<E, K, SILU, true><<<grid, block, 0, s>>>(a);
     else conv_bwd_kernel<E, K, SILU, false><<<grid, block, 0, s>>>(a);
 }
@@ -225,7 +230,7 @@ template <class E, int K>
 hipError_t launch_k(const CArgs& a, const ConvBwdLaunch& l, hipStream_t s) {
     if (l.silu) launch_v<E, K, true>(a, l.vec_ok, s);
     else launch_v<E, K, false>(a, l.vec_ok, s);
-    if (a.S > 1) conv_sums_kernel<K><<<dim3(blocks_for(a.Dn * (K + 1), 256)), dim3(256), 0, s>>>(a.part, l.dw, l.db, a.Dn, a.R / a.Dn,
+    if (a.part || a.R == 0) conv_sums_kernel<K><<<dim3(blocks_for(a.Dn * (K + 1), 4)), dim3(256), 0, s>>>(a.part, l.dw, l.db, a.Dn, a.R / a.Dn,
                                                                                   a.S);
     return hipGetLastError();
 }
@@ -243,16 +248,17 @@ hipError_t launch_e(const CArgs& a, const ConvBwdLaunch& l, hipStream_t s) {
 }  // namespace
 
 int64_t conv1d_bwd_scratch(int64_t Bt, int64_t Dn, int64_t L, int64_t K) {
-    const int S = plan_of(Bt * Dn, L).S;
-    return S > 1 ? (K + 1) * Bt * Dn * S : 0;
+    const Plan p = plan_of(Bt * Dn, L);
+    return p.parts(Bt, Dn) ? (K + 1) * Bt * Dn * p.S : 0;
 }
 
 hipError_t launch_conv1d_bwd(const ConvBwdLaunch& l, hipStream_t s) {
     const Plan p = plan_of(l.R, l.L);
     CArgs a{};
     a.x = l.x; a.w = l.w; a.bias = l.bias; a.st = l.state_in; a.dout = l.dout; a.dfin = l.dfinal; a.dx = l.dx;
-    a.dst = l.dstate; a.dw = l.dw; a.db = l.db; a.part = l.scratch; a.Dn = l.Dn; a.L = l.L; a.R = l.R;
+    a.dst = l.dstate; a.dw = l.dw; a.db = l.db; a.Dn = l.Dn; a.L = l.L; a.R = l.R;
     a.Bt = l.R / l.Dn;
+    a.part = p.parts(a.Bt, l.Dn) ? l.scratch : nullptr;
     a.tiles = p.tiles; a.seg_tiles = p.seg_tiles; a.S = p.S;
     return l.bf16 ? launch_e<BF16>(a, l, s) : launch_e<F32>(a, l, s);
 }

@@ -76,12 +76,14 @@ __device__ __forceinline__ Row row_of(float rate) {
     for (int k = 0; k < 5; ++k) w.c[k] = kQ[k] * p, p *= 2.0f * rate;
     return w;
 }
+__device__ __forceinline__ float q_of(float y, float a) {
+    const float t = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, kQ[4], kQ[3]), kQ[2]), kQ[1]), kQ[0]);
+    return y < 0.5f ? t : fmaf(-a, a, 1.0f);
+}
 template <bool SMALL>
 __device__ __forceinline__ float q_of(const Row& w, float r, float a) {
     if (SMALL) return r * fmaf(r, fmaf(r, fmaf(r, fmaf(r, w.c[4], w.c[3]), w.c[2]), w.c[1]), w.c[0]);
-    const float y = 2.0f * w.rate * r;
-    const float t = y * fmaf(y, fmaf(y, fmaf(y, fmaf(y, kQ[4], kQ[3]), kQ[2]), kQ[1]), kQ[0]);
-    return y < 0.5f ? t : fmaf(-a, a, 1.0f);
+    return q_of(2.0f * w.rate * r, a);
 }
 __device__ __forceinline__ float exp_neg(float v) { return fast_exp2(v * -kLog2e); }
 
@@ -398,6 +400,7 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
             if (FOLD) a.seg[row * a.S + seg] = make_float2(all_p, g);
             else if (a.dh0 && first == 0) a.dh0[row] = g;
         }
+        if (W > 1) __syncthreads();  // the next pass writes sh
         return FOLD ? 0.0f : wave_sum(drate);
     };
     // the waves' parts added in order, for the wave that leads `ways` of them
@@ -410,43 +413,55 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
         __syncthreads();
         return s;
     };
+    const bool parts = FOLD || a.drate_part;  // an item is a row's segment, else a channel
     if (W == 1) {
-        const int ways = channel_ways(a.Bt), channels = 4 / ways, lead = at.item % ways;
-        for (int64_t c = (int64_t)blockIdx.x * channels; c < a.Dn; c += (int64_t)gridDim.x * channels) {
-            const int64_t ch = c + at.item / ways;
+        const int ways = parts ? 1 : channel_ways(a.Bt), channels = 4 / ways, lead = at.item % ways;
+        const int64_t items = parts ? a.R : a.Dn, rows = parts ? 1 : a.Bt;
+        for (int64_t c = (int64_t)blockIdx.x * channels; c < items; c += (int64_t)gridDim.x * channels) {
+            const int64_t it = c + at.item / ways;
             float part = 0.0f;
-            if (ch < a.Dn)
-                for (int64_t b = lead; b < a.Bt; b += ways) part += pass(b * a.Dn + ch, 0);
+            if (it < items)
+                for (int64_t b = lead; b < rows; b += ways) part += pass(b * a.Dn + it, 0);
             part = total(at.item, ways, part);
-            if (ch < a.Dn && lead == 0 && at.lane == 0) a.drate[ch] = part;
+            if (it < items && lead == 0 && at.lane == 0) (parts ? a.drate_part : a.drate)[it] = part;
         }
     } else {
-        for (int64_t it = blockIdx.x; it < a.R * a.S; it += gridDim.x) {
-            const float part = total(at.wave, W, pass(it / a.S, static_cast<int>(it % a.S)));
-            if (!FOLD && at.lane == 0 && at.wave == 0) (a.drate_part ? a.drate_part : a.drate)[it] = part;
+        const int64_t items = parts ? a.R * a.S : a.Dn, rows = parts ? 1 : a.Bt;
+        for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+            float part = 0.0f;
+            for (int64_t b = 0; b < rows; ++b)
+                part += pass(parts ? it / a.S : b * a.Dn + it, parts ? static_cast<int>(it % a.S) : 0);
+            part = total(at.wave, W, part);
+            if (!FOLD && at.lane == 0 && at.wave == 0) (parts ? a.drate_part : a.drate)[it] = part;
         }
     }
 }
 
-// drate[d] = sum over the rows of channel d and their segments, in order.
+// drate[d] = sum over the rows of channel d and their segments: a wave per channel, each lane every 64th
+// part in order, then the lanes.
 __global__ __launch_bounds__(256) void gated_rate_kernel(const float* part, float* drate, int64_t Dn, int64_t Bt, int S) {
-    for (int64_t d = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; d < Dn; d += (int64_t)gridDim.x * blockDim.x) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t d = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); d < Dn; d += (int64_t)gridDim.x * 4) {
         float s = 0.0f;
-        for (int64_t b = 0; b < Bt; ++b)
-            for (int k = 0; k < S; ++k) s += part[(b * Dn + d) * S + k];
-        drate[d] = s;
+        for (int64_t n = lane; n < Bt * S; n += 64) s += part[(n / S * Dn + d) * S + n % S];
+        s = wave_sum(s);
+        if (lane == 0) drate[d] = s;
     }
 }
 
-template <class E>
+// One token, a thread per channel of a row (four to a thread with wide loads took the same 3.1 us for 64 x
+// 5120 bf16: the step is a launch and a round trip to memory).  I: a 32-bit index where it will do, whose
+// division is far shorter.
+template <class E, class I>
 __global__ __launch_bounds__(256) void gated_step_kernel(float* state, const void* x, const void* f, const void* i,
                                                          const float* rate, void* out, int64_t Dn, int64_t R) {
-    for (int64_t n = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; n < R; n += (int64_t)gridDim.x * blockDim.x) {
-        const Row w = row_of(rate[n % Dn]);
+    for (I k = static_cast<I>(blockIdx.x) * 256 + static_cast<I>(threadIdx.x); k < static_cast<I>(R);
+         k += static_cast<I>(gridDim.x) * 256) {
+        const int64_t n = static_cast<int64_t>(k);
+        const float rt = rate[k % static_cast<I>(Dn)];
         const float r = fast_rcp(1.0f + exp_neg(E::load1(f, n))), p = fast_rcp(1.0f + exp_neg(E::load1(i, n)));
-        const float av = fast_exp2(r * w.nrl);
-        const float m = __builtin_amdgcn_sqrtf(q_of<false>(w, r, av));
-        const float h = fmaf(av, state[n], m * p * E::load1(x, n));
+        const float av = fast_exp2(-rt * r * kLog2e);
+        const float h = fmaf(av, state[n], __builtin_amdgcn_sqrtf(q_of(2.0f * rt * r, av)) * p * E::load1(x, n));
         state[n] = h;
         E::store1(out, n, h);
     }
@@ -456,8 +471,11 @@ __global__ __launch_bounds__(256) void gated_step_kernel(float* state, const voi
 struct Plan {
     int W, S;
     int64_t tiles, seg_tiles;
-    // whether the backward leaves parts of drate for a second kernel to add up
-    bool parts(int64_t Bt) const { return S > 1 || (W > 1 && Bt > 1); }
+    // Whether the backward leaves parts of drate for a second kernel to add up (4.7 us); otherwise a block takes
+    // a channel's rows in turn (3 x 1531 x 2041 f32: 57 us, 61 in parts).
+    bool parts(int64_t Bt, int64_t Dn) const {
+        return S > 1 || (W == 1 ? goes_by_parts(Bt, Dn, channel_ways(Bt), channel_ways(Bt)) : goes_by_parts(Bt, Dn, W, 1));
+    }
 };
 // Four waves to a row read it in longer runs and hand the map on; they pay where a row has at least two
 // rounds for them (bf16) or one (f32, whose rounds move twice the bytes).  Rows of 16-bit elements that
@@ -499,7 +517,7 @@ GArgs args_of(const GatedLaunch& l, const Plan& p) {
     a.Bt = l.Bt; a.drate = l.drate;
     a.tiles = p.tiles; a.seg_tiles = p.seg_tiles; a.S = p.S;
     a.seg = reinterpret_cast<float2*>(l.scratch);  // R S maps when S > 1, then R S parts of drate
-    a.drate_part = p.parts(l.Bt) ? l.scratch + (p.S > 1 ? 2 * a.R * p.S : 0) : nullptr;
+    a.drate_part = p.parts(l.Bt, l.Dn) ? l.scratch + (p.S > 1 ? 2 * a.R * p.S : 0) : nullptr;
     return a;
 }
 
@@ -508,11 +526,12 @@ void run_w(const GArgs& a, bool bwd, hipStream_t s) {
     const dim3 grid(blocks_for(a.R * a.S, Place<W>::kRows)), block(Place<W>::kThreads);
     if (bwd) {
         if constexpr (W == 1) {
-            const dim3 channels(blocks_for(a.Dn, 4 / channel_ways(a.Bt)));
+            const dim3 channels = a.drate_part ? grid : dim3(blocks_for(a.Dn, 4 / channel_ways(a.Bt)));
             gated_bwd_kernel<E, VEC, 1, false><<<channels, block, 0, s>>>(a);
         } else {
             if (a.S > 1) gated_bwd_kernel<E, VEC, W, true><<<grid, block, 0, s>>>(a);
-            gated_bwd_kernel<E, VEC, W, false><<<grid, block, 0, s>>>(a);
+            const dim3 rows = a.drate_part ? grid : dim3(blocks_for(a.Dn, 1));
+            gated_bwd_kernel<E, VEC, W, false><<<rows, block, 0, s>>>(a);
         }
     } else {
         if constexpr (W > 1)
@@ -528,7 +547,7 @@ void run_v(const GArgs& a, int W, bool bwd, hipStream_t s) {
 }
 hipError_t run(const GatedLaunch& l, bool bwd, hipStream_t s) {
     if (l.Bt * l.Dn == 0) {  // no rows: drate alone is written, with zeros
-        if (bwd) gated_rate_kernel<<<dim3(blocks_for(l.Dn, 256)), dim3(256), 0, s>>>(nullptr, l.drate, l.Dn, 0, 1);
+        if (bwd) gated_rate_kernel<<<dim3(blocks_for(l.Dn, 4)), dim3(256), 0, s>>>(nullptr, l.drate, l.Dn, 0, 1);
         return hipGetLastError();
     }
     const Plan p = plan_of(l.Bt * l.Dn, l.L, l.bf16, l.vec_ok);
@@ -538,7 +557,7 @@ hipError_t run(const GatedLaunch& l, bool bwd, hipStream_t s) {
         else l.vec_ok ? run_v<F32, true>(a, p.W, bwd, s) : run_v<F32, false>(a, p.W, bwd, s);
     }
     if (bwd && a.drate_part)
-        gated_rate_kernel<<<dim3(blocks_for(a.Dn, 256)), dim3(256), 0, s>>>(a.drate_part, l.drate, a.Dn, l.Bt, p.S);
+        gated_rate_kernel<<<dim3(blocks_for(a.Dn, 4)), dim3(256), 0, s>>>(a.drate_part, l.drate, a.Dn, l.Bt, p.S);
     return hipGetLastError();
 }
 
@@ -557,7 +576,7 @@ int64_t gated_bwd_scratch(int64_t Bt, int64_t Dn, int64_t L) {
     int64_t n = 0;
     for (int k = 0; k < 4 && Bt * Dn > 0; ++k) {
         const Plan p = plan_of(Bt * Dn, L, k & 1, k & 2);
-        n = std::max(n, Bt * Dn * ((p.S > 1 ? 2 * p.S : 0) + (p.parts(Bt) ? p.S : 0)));
+        n = std::max(n, Bt * Dn * ((p.S > 1 ? 2 * p.S : 0) + (p.parts(Bt, Dn) ? p.S : 0)));
     }
     return n;
 }
@@ -567,8 +586,10 @@ hipError_t launch_gated_bwd(const GatedLaunch& l, hipStream_t s) { return run(l,
 
 hipError_t launch_gated_update(const GatedUpdateLaunch& l, hipStream_t s) {
     const dim3 grid(blocks_for(l.R, 256)), block(256);
-    if (l.bf16) gated_step_kernel<BF16><<<grid, block, 0, s>>>(l.state, l.x, l.f, l.i, l.rate, l.out, l.Dn, l.R);
-    else gated_step_kernel<F32><<<grid, block, 0, s>>>(l.state, l.x, l.f, l.i, l.rate, l.out, l.Dn, l.R);
+    const auto go = [&](auto kernel) { kernel<<<grid, block, 0, s>>>(l.state, l.x, l.f, l.i, l.rate, l.out, l.Dn, l.R); };
+    const bool small = l.R < int64_t{1} << 31;
+    if (l.bf16) small ? go(gated_step_kernel<BF16, uint32_t>) : go(gated_step_kernel<BF16, int64_t>);
+    else small ? go(gated_step_kernel<F32, uint32_t>) : go(gated_step_kernel<F32, int64_t>);
     return hipGetLastError();
 }
 

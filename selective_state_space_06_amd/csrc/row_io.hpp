@@ -132,8 +132,12 @@ __device__ __forceinline__ void store8(typename E::storage* p, int rem, int lane
 
 // How the four waves of a block share channels when a sum over the batch is wanted: `ways` waves to a
 // channel, each with every ways-th batch, joined through LDS in order; one launch then gives the sum,
-// where partial sums per row and a second kernel took 4 us more.
+// where partial sums per row and a second kernel take 4 to 5 us more.  A batch that leaves too few waves
+// that way (under 4096, four a SIMD) goes by rows and parts.
 __host__ __device__ inline int channel_ways(int64_t batch) { return batch == 1 ? 1 : batch == 2 ? 2 : 4; }
+inline bool goes_by_parts(int64_t batch, int64_t channels, int waves_per_channel, int rows_at_once) {
+    return batch > rows_at_once && channels * waves_per_channel < 4096;
+}
 
 // Blocks for n items, `per` a block; kernels stride over what a capped grid leaves.
 inline unsigned blocks_for(int64_t n, int64_t per) {

@@ -94,6 +94,10 @@ def test_ties_go_by_beam_then_logit_then_token(mss):  # noqa: F811
     s = np.array([[-3, -1, -7, -1, -2, -1]] * 2, np.float32)
     run_and_check(mss, x, s, "f32", 24)
     run_and_check(mss, x, s, "bf16", 24)
+    zeros = np.zeros((1, 3, 2000), np.float32)  # zeros of both signs are equal
+    zeros[:, :, ::3] = -0.0
+    run_and_check(mss, zeros, np.array([[-1, -0.0, 0.0]], np.float32), "f32", 40)
+    run_and_check(mss, zeros, np.array([[-1, -0.0, 0.0]], np.float32), "bf16", 40)
     up = np.arange(30000, dtype=np.float32)[None, None] * 1e-3  # every tile beats the list
     x = np.concatenate([up, up[..., ::-1]], 1)
     got = run_and_check(mss, x, np.zeros((1, 2), np.float32), "f32", 32, mixed=True)

@@ -51,7 +51,9 @@ def check_all(c, g, silu, states, bias, what):
     (2, 64, 256, 4, "f32"), (2, 64, 256, 4, "bf16"), (1, 7, 1, 4, "f32"), (2, 5, 2, 4, "bf16"), (1, 3, 3, 3, "f32"),
     (3, 5, 17, 4, "bf16"), (2, 48, 511, 3, "f32"), (2, 48, 512, 2, "bf16"), (1, 32, 513, 1, "f32"),
     (2, 6, 515, 4, "bf16"), (1, 3, 514, 4, "f32"), (4, 100, 1000, 4, "bf16"), (1, 2, 30001, 4, "f32"),
-    (1, 1, 40960, 4, "bf16"), (5, 33, 1537, 2, "f32")])
+    (1, 1, 40960, 4, "bf16"), (5, 33, 1537, 2, "f32"),
+    (300, 3, 50, 4, "f32"), (9000, 1, 30, 3, "bf16"), (6, 1030, 90, 4, "f32"), (2, 4100, 700, 4, "bf16"),
+    (1, 8200, 40, 2, "f32"), (3, 2731, 520, 4, "bf16")])
 @pytest.mark.parametrize("states,silu,bias", [(False, True, True), (True, True, False), (True, False, True)])
 def test_conv_gradients(mss, B, D, L, K, dtype, states, silu, bias):  # noqa: F811
     import torch

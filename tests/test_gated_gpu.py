@@ -101,7 +101,9 @@ def check_grads(c, g, what):
 SHAPES = [(2, 64, 256, "f32"), (2, 64, 256, "bf16"), (1, 3, 1, "f32"), (1, 5, 1, "bf16"), (3, 5, 7, "f32"),
           (2, 70, 511, "bf16"), (2, 70, 512, "bf16"), (2, 7, 513, "f32"), (1, 1, 2047, "f32"), (2, 33, 1500, "bf16"),
           (1, 9, 5000, "f32"), (2, 11, 4104, "bf16"), (1, 2, 20001, "f32"), (1, 1, 40960, "bf16"),
-          (1, 130, 9000, "f32")]
+          (1, 130, 9000, "f32"), (1, 3, 70001, "f32"), (2, 20, 66048, "bf16"), 
+          (3, 1030, 4097, "f32"), (2, 2100, 1100, "f32"), (1, 5000, 600, "bf16"),
+          (300, 3, 50, "f32"), (2100, 2, 40, "bf16"), (700, 3, 1100, "f32"), (6, 1030, 90, "f32")]
 
 
 @pytest.mark.parametrize("B,D,L,dtype", SHAPES)

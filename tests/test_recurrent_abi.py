@@ -245,6 +245,7 @@ def test_reorder_refusals():
     assert raw(ok + [strided(T([B * 4, 8]))], par, None) == LAYOUT
     assert raw(ok + [moved(T([B * 4, 8]), 2)], par, None) == LAYOUT
     assert raw(ok + [moved(ok[0], 16)], par, None) == ALIAS
+    assert raw([ok[0], ok[0]], par, None) == ALIAS  # the same state twice would be moved twice
     big = T([B * 4, 8])
     assert raw([big], Tensor.make(big.data + 32, MSS_I32, [B, 4]), None) == ALIAS
     assert raw([T([B * 65, 4])], T([B, 65], MSS_I32), None) == UNSUPPORTED

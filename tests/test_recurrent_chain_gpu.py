@@ -127,3 +127,51 @@ def test_beam_search_decodes_the_model(mss):  # noqa: F811
         # 2e-5), added up in the scores
         assert np.abs(scores.cpu().numpy() - rs)[np.isfinite(rs)].max() < 1e-4 * (t + 1), t
         assert np.abs(host64(h) - rh).max() < 1e-4 and np.abs(host64(win) - rwin).max() < 1e-6, t
+
+
+def test_two_host_threads(mss):  # noqa: F811
+    """Every operator from two host threads at once, each on a stream of its own: nothing is shared, so each
+    thread gets what the calls give alone, bit for bit."""
+    import threading
+
+    import torch
+
+    def inputs(k):
+        g = torch.Generator(device="cuda").manual_seed(k)
+        n = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+        return dict(x=n(2, 70, 1500), f=n(2, 70, 1500), i=n(2, 70, 1500), d=n(2, 70, 1500), rate=n(70).abs() * 0.1 + 0.01,
+                    w=n(70, 4), logits=n(3, 5, 4000), scores=n(3, 5), st=n(15, 33, 16),
+                    par=torch.randint(0, 5, (3, 5), generator=g, device="cuda", dtype=torch.int32))
+
+    def work(t):
+        out, last, saved = mss.gated_scan_fwd_save(t["x"], t["f"], t["i"], t["rate"])
+        g = mss.gated_scan_bwd(t["x"], t["f"], t["i"], t["rate"], t["d"], saved_states=saved)
+        c = mss.causal_conv1d_bwd(t["x"], t["w"], t["d"])
+        sel = mss.beam_select(t["logits"], t["scores"])
+        st = mss.beam_reorder([t["st"].clone()], t["par"])[0]
+        up = last.clone()
+        o = mss.gated_state_update(up, t["x"][..., 0].contiguous(), t["f"][..., 0].contiguous(),
+                                   t["i"][..., 0].contiguous(), t["rate"])
+        return [out, last, *g.values(), *c.values(), *sel, st, up, o]
+
+    ts = [inputs(k) for k in range(2)]
+    want = [[v.clone() for v in work(t)] for t in ts]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = work(ts[k])
+                    torch.cuda.current_stream().synchronize()
+                    if not all(torch.equal(a, b) for a, b in zip(got, want[k])):
+                        wrong.append(k)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # an assertion in a thread would be lost
+            wrong.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not wrong, wrong
