@@ -153,7 +153,7 @@ def gated_scan_fwd(x, fgate, igate, rate, initial_state=None, seq_lens=None, ret
     h_t = a h_{t-1} + sqrt(1 - a^2) sigmoid(igate_t) x_t with a = exp(-rate sigmoid(fgate_t)), out = h.
 
     x, fgate, igate: (batch, d_inner, L) float32 or bfloat16 (the gates before their sigmoid); rate:
-    (d_inner,) float32, positive; initial_state: (batch, d_inner) float32 (None: zeros); seq_lens:
+    (d_inner,) float32, positive and finite; initial_state: (batch, d_inner) float32 (None: zeros); seq_lens:
     (batch,) int32 on the device (None: all L; outputs past a sequence's end are 0).  Returns out (dtype
     of x), or (out, last_state) with last_state (batch, d_inner) float32."""
     import torch
@@ -391,7 +391,8 @@ class BeamSearchStep:
     """One step of a beam search bound to fixed device buffers: mss_beam_select on `logits` with
     `scores` (and `finished`) updated in place, then mss_beam_reorder of `states` by the parents it
     chose.  Arguments as for beam_select and beam_reorder; calling it returns (parents, tokens), its own
-    (batch, beams) int32 buffers, which the next call overwrites."""
+    (batch, beams) int32 buffers, which the next call overwrites.  Without `finished` a beam that takes
+    end_token goes on like any other."""
 
     def __init__(self, logits, scores, states, finished=None, end_token=None, stream=None):
         import torch

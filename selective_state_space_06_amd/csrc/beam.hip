@@ -401,8 +401,8 @@ void reorder_u(RArgs& a, hipStream_t s) {
 }
 
 // Slices per row: blocks for every CU twice over (64 x 8 x 128008 f32: 59 us; four times 68, eight times 64:
-// each wave fills a list of its own), each wave with a tile, and lists that fit the merging block's
-// shared memory.
+// each wave fills a list of its own; four times with four waves a block 61), each wave with a tile, and
+// lists that fit the merging block's shared memory.
 constexpr int64_t kMergeBytes = 56 << 10;
 void plan_select(int64_t rows, int64_t N, int64_t V, int64_t K, int64_t* per, int* slices) {
     const int64_t tiles = (V + kTile - 1) / kTile;

@@ -230,8 +230,8 @@ template <class E, int K>
 hipError_t launch_k(const CArgs& a, const ConvBwdLaunch& l, hipStream_t s) {
     if (l.silu) launch_v<E, K, true>(a, l.vec_ok, s);
     else launch_v<E, K, false>(a, l.vec_ok, s);
-    if (a.part || a.R == 0) conv_sums_kernel<K><<<dim3(blocks_for(a.Dn * (K + 1), 4)), dim3(256), 0, s>>>(a.part, l.dw, l.db, a.Dn, a.R / a.Dn,
-                                                                                  a.S);
+    if (a.part)
+        conv_sums_kernel<K><<<dim3(blocks_for(a.Dn * (K + 1), 4)), dim3(256), 0, s>>>(a.part, l.dw, l.db, a.Dn, a.Bt, a.S);
     return hipGetLastError();
 }
 

@@ -552,10 +552,8 @@ hipError_t run(const GatedLaunch& l, bool bwd, hipStream_t s) {
     }
     const Plan p = plan_of(l.Bt * l.Dn, l.L, l.bf16, l.vec_ok);
     const GArgs a = args_of(l, p);
-    {
-        if (l.bf16) l.vec_ok ? run_v<BF16, true>(a, p.W, bwd, s) : run_v<BF16, false>(a, p.W, bwd, s);
-        else l.vec_ok ? run_v<F32, true>(a, p.W, bwd, s) : run_v<F32, false>(a, p.W, bwd, s);
-    }
+    if (l.bf16) l.vec_ok ? run_v<BF16, true>(a, p.W, bwd, s) : run_v<BF16, false>(a, p.W, bwd, s);
+    else l.vec_ok ? run_v<F32, true>(a, p.W, bwd, s) : run_v<F32, false>(a, p.W, bwd, s);
     if (bwd && a.drate_part)
         gated_rate_kernel<<<dim3(blocks_for(a.Dn, 4)), dim3(256), 0, s>>>(a.drate_part, l.drate, a.Dn, l.Bt, p.S);
     return hipGetLastError();

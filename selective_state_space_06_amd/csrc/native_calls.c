@@ -162,9 +162,9 @@ static PyObject* beam_reorder(PyObject* self, PyObject* const* args, Py_ssize_t 
         PyErr_SetString(PyExc_TypeError, "states, parents and a stream wanted");
         return NULL;
     }
-    PyObject* seq = PySequence_Fast(args[0], "states: a sequence of tensors");
+    PyObject* seq = PySequence_Tuple(args[0]); /* of its own: no other thread changes it meanwhile */
     if (!seq) return NULL;
-    const Py_ssize_t k = PySequence_Fast_GET_SIZE(seq);
+    const Py_ssize_t k = PyTuple_GET_SIZE(seq);
     PyObject* result = NULL;
     mss_tensor_t par, *d = PyMem_Malloc((size_t)(k + 1) * sizeof *d);
     const mss_tensor_t** p = PyMem_Malloc((size_t)(k + 1) * sizeof *p);
@@ -175,7 +175,7 @@ static PyObject* beam_reorder(PyObject* self, PyObject* const* args, Py_ssize_t 
     }
     if (describe(args[1], &par, &device)) goto done;
     for (Py_ssize_t j = 0; j < k; ++j) {
-        if (describe(PySequence_Fast_GET_ITEM(seq, j), &d[j], &device)) goto done;
+        if (describe(PyTuple_GET_ITEM(seq, j), &d[j], &device)) goto done;
         p[j] = &d[j];
     }
     void* stream = (void*)(uintptr_t)PyLong_AsUnsignedLongLong(args[2]);
