@@ -265,10 +265,10 @@ __global__ __launch_bounds__(Place<W>::kThreads) void gated_fwd_kernel(GArgs a) 
             store8<E, VEC>(static_cast<S*>(a.out) + row * a.L + t, rem, at.lane, v);
         };
         const int64_t inside = w.small ? len / kTile : 0;  // tiles a fast round may end at
-        for (int64_t k0 = first; k0 < end; k0 += W) {
-            if (k0 + W <= inside && k0 + W <= end) round(k0, True{});
-            else round(k0, False{});
-        }
+        const int64_t fast = inside < end ? inside : end;
+        int64_t k0 = first;
+        for (; k0 + W <= fast; k0 += W) round(k0, True{});
+        for (; k0 < end; k0 += W) round(k0, False{});
         if (at.lane == 0 && at.wave == 0) {
             if (FOLD) a.seg[it] = make_float2(all_p, h);
             else if (a.last && end == a.tiles) a.last[row] = h;
