@@ -9,7 +9,8 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import MssError, Tensor, _bound_stream, _desc, _ref, load_library
+from ._binding import (
+    MssError, Tensor, _bound_stream, _desc, _note_written, _ref, _refuse_written, load_library)
 
 SAVED_SPACING = 512  # steps between two of gated_scan_fwd_save's states
 
@@ -157,11 +158,14 @@ def gated_scan_fwd(x, fgate, igate, rate, initial_state=None, seq_lens=None, ret
     (batch,) int32 on the device (None: all L; outputs past a sequence's end are 0).  Returns out (dtype
     of x), or (out, last_state) with last_state (batch, d_inner) float32."""
     import torch
+    given = (out, last_state)
+    _refuse_written(*given)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if return_last_state and last_state is None:
         last_state = torch.empty(x.shape[:2], dtype=torch.float32, device=x.device)
     _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, out, last_state if return_last_state else None, None)
+    _note_written(*given)
     return (out, last_state) if return_last_state else out
 
 
@@ -171,6 +175,8 @@ def gated_scan_fwd_save(x, fgate, igate, rate, initial_state=None, seq_lens=None
     (batch, d_inner, ceil(L / 512)) float32, the state entering every 512th step.  Returns
     (out, last_state, saved_states)."""
     import torch
+    given = (out, last_state, saved_states)
+    _refuse_written(*given)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if last_state is None:
@@ -178,6 +184,7 @@ def gated_scan_fwd_save(x, fgate, igate, rate, initial_state=None, seq_lens=None
     if saved_states is None:
         saved_states = _saved_like(x)
     _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, out, last_state, saved_states)
+    _note_written(*given)
     return out, last_state, saved_states
 
 
@@ -207,9 +214,11 @@ def gated_state_update(state, x, fgate, igate, rate, out=None):
     (batch, d_inner) float32 is updated in place.  x, fgate, igate: (batch, d_inner) float32 or
     bfloat16.  Returns out (batch, d_inner) in x's dtype."""
     import torch
+    _refuse_written(state, out)
     if out is None:
         out = torch.empty_like(x)
     _launch("gated_state_update", x, state, x, fgate, igate, rate, out)
+    _note_written(state, out)
     return out
 
 
@@ -245,6 +254,8 @@ def beam_select(logits, scores, finished=None, end_token=None, k=None, next_scor
     float32, parents int32, tokens int32), each (batch, k), best first, and with `finished` given also
     next_finished int32.  next_scores=scores and next_finished=finished update those in place."""
     import torch
+    given = (next_scores, parents, tokens, next_finished)
+    _refuse_written(*given)
     # outputs after the model of scores where they have its shape (empty_like takes half the time of empty)
     shape = (logits.shape[0], scores.shape[-1] if k is None else int(k))
     like = scores if scores.shape == shape else scores.new_empty(shape)
@@ -260,6 +271,7 @@ def beam_select(logits, scores, finished=None, end_token=None, k=None, next_scor
     floats = beam_select_scratch(*logits.shape, shape[1]) if ok else 0
     _launch("beam_select", logits, logits, scores, finished, -1 if end_token is None else int(end_token), next_scores,
             parents, tokens, next_finished, _scratch(floats, logits.device))
+    _note_written(*given)
     got = (next_scores, parents, tokens)
     return got if next_finished is None else got + (next_finished,)
 
@@ -269,7 +281,10 @@ def beam_reorder(states, parents):
     parents[b, j] (mss_beam_reorder), on the current stream.  states: a sequence of float32, bfloat16 or
     int32 tensors (all layers' scan states and conv windows in one call); parents: (batch, beams) int32;
     a parent outside [0, beams) leaves its row as it is.  Returns states."""
-    _launch("beam_reorder", parents, states, parents)
+    given = tuple(states)
+    _refuse_written(*given)
+    _launch("beam_reorder", parents, given, parents)
+    _note_written(*given)
     return states
 
 
@@ -288,7 +303,8 @@ class GatedScanFunction:
     """torch.autograd wrapper of the gated scan: GatedScanFunction.apply(x, fgate, igate, rate,
     initial_state, seq_lens) -> (out, last_state), differentiable in x, fgate, igate, rate and
     initial_state (initial_state, seq_lens may be None).  The forward keeps one state in 512 for the
-    backward.  To capture a training step in a graph, capture gated_scan_fwd_save and gated_scan_bwd:
+    backward.  Decoding goes on from last_state.detach().clone(): the calls that write a state in place
+    refuse one that requires gradients.  To capture a training step in a graph, capture gated_scan_fwd_save and gated_scan_bwd:
     autograd ends the process when it captures a backward of leaves that an eager graph still holds."""
 
     @staticmethod
@@ -374,6 +390,7 @@ class GatedUpdateStep:
     gated_state_update; calling it updates `state` in place and writes `out` (returned)."""
 
     def __init__(self, state, x, fgate, igate, rate, out=None, stream=None):
+        _refuse_written(state, out)
         _same_device(x, (state, fgate, igate, rate, out))
         stream = _bound_stream(x, stream)
         self.out = _empty_on(stream, x.shape, x.dtype, x.device) if out is None else out
@@ -384,6 +401,7 @@ class GatedUpdateStep:
 
     def __call__(self):
         _raise(self._fn(*self._args), "mss_gated_state_update")
+        _note_written(self._keep[0], self.out)
         return self.out
 
 
@@ -396,6 +414,8 @@ class BeamSearchStep:
 
     def __init__(self, logits, scores, states, finished=None, end_token=None, stream=None):
         import torch
+        states = tuple(states)
+        _refuse_written(scores, finished, *states)
         _same_device(logits, (scores, finished, *states))
         stream = _bound_stream(logits, stream)
         self.parents = _empty_on(stream, scores.shape, torch.int32, logits.device)
@@ -403,6 +423,7 @@ class BeamSearchStep:
         floats = beam_select_scratch(*logits.shape, scores.shape[-1])
         scratch = _empty_on(stream, (floats,), torch.float32, logits.device)
         self._keep = (logits, scores, finished, self.parents, self.tokens, scratch, *states)
+        self._written = (scores, finished, self.parents, self.tokens, *states)
         lo, sc, fi, pa, to, scr, *sts = [_desc(t) for t in self._keep]
         self._descs = (lo, sc, fi, pa, to, scr, sts)
         self._select_args = (_ref(lo), _ref(sc), _ref(fi), -1 if end_token is None else int(end_token), _ref(sc),
@@ -413,4 +434,5 @@ class BeamSearchStep:
     def __call__(self):
         _raise(self._lib.mss_beam_select(*self._select_args), "mss_beam_select")
         _raise(self._lib.mss_beam_reorder(*self._reorder_args), "mss_beam_reorder")
+        _note_written(*self._written)
         return self.parents, self.tokens
