@@ -408,8 +408,10 @@ int mss_ssd_scan_fwd(const mss_tensor_t* x, const mss_tensor_t* dt, const mss_te
  *   saved_states     (batch, d_inner, ceil(L / 512)) f32, written with the state entering step 512 k,
  *                                          for the backward; nullable
  * At least one output (MSS_ERR_NULL_ARG).  No output may overlap an input or another output.
- * Arithmetic and state are fp32; a row's inputs that are not finite make its later outputs not
- * finite (infinite or NaN).  Rows that are whole aligned 16-byte vectors take aligned accesses,
+ * Arithmetic and state are fp32.  A NaN, or an infinite x or initial_state, makes the row's outputs not
+ * finite (infinite or NaN) from its step on.  An infinite gate is its sigmoid's limit: fgate at -inf
+ * holds the state and lets nothing in, at +inf decays by exp(-rate); igate at -inf lets nothing in, at
+ * +inf all of sqrt(1 - a^2) x.  Rows that are whole aligned 16-byte vectors take aligned accesses,
  * others element-aligned ones.
  */
 int mss_gated_scan_scratch(int64_t batch, int64_t d_inner, int64_t L, int64_t* fwd_floats, int64_t* bwd_floats);
@@ -429,6 +431,8 @@ int mss_gated_scan_fwd(const mss_tensor_t* x, const mss_tensor_t* fgate, const m
  *   dx, dfgate, digate   (batch, d_inner, L)  dtype of x, written (0 past a sequence's end)
  *   drate                (d_inner,)           f32, written (sum over batch and time, fixed order)
  *   dinitial_state       (batch, d_inner)     f32, nullable, written
+ * A NaN reaches the gradients whose formula it stands in.  At a closed gate (fgate -inf) dx, dfgate and
+ * digate are 0 for |x| up to 1e19.
  */
 int mss_gated_scan_bwd(const mss_tensor_t* x, const mss_tensor_t* fgate, const mss_tensor_t* igate,
                        const mss_tensor_t* rate, const mss_tensor_t* seq_lens,

@@ -63,8 +63,8 @@ struct Row {
     float c[5];       // kQ[k] (2 rate)^(k + 1)
     bool small;
 };
-// The least q: keeps 1 / m finite where the gate is closed (r = 0, m = 0; m is then 2^-62, and a normal number,
-// which a reciprocal root takes).
+// The least q under 1 / m, which it keeps finite where the gate is closed (r = 0, m = 0; 1 / m is then 2^62), and
+// a normal number, which a reciprocal root takes.
 constexpr float kLeastQ = 0x1p-124f;
 __device__ __forceinline__ Row row_of(float rate) {
     Row w;
@@ -341,13 +341,13 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
                     // 1 - sigmoid without its cancellation; where e^-f overflows the product is inf * 0 and the
                     // minimum picks its limit, 1
                     const float x = xc[e], ei = exp_neg(pm[e]), p = fast_rcp(1.0f + ei);
-                    const float q = fmaxf(q_of<FAST>(w, rv[e], av[e]), kLeastQ);
-                    float im = __builtin_amdgcn_rsqf(q);  // 1 / m
+                    const float q = q_of<FAST>(w, rv[e], av[e]);
+                    float im = __builtin_amdgcn_rsqf(fmaxf(q, kLeastQ));  // 1 / m
                     if (!FAST) im = w.rate == 0.0f ? 0.0f : im;
                     sc[e] = w.rate * rv[e] * fminf(ef * rv[e], 1.0f);
                     xc[e] = x * fminf(ei * p, 1.0f);
                     into[e] = av[e] * av[e] * im * (p * x);
-                    pm[e] = p * (q * im);
+                    pm[e] = p * (q * im);  // q as it is: 0 of a closed gate stays 0, and a NaN, which fmaxf drops, a NaN
                     v[e] = pm[e] * x;
                     if (off) rv[e] = sc[e] = xc[e] = into[e] = pm[e] = v[e] = 0.0f;
                 }
