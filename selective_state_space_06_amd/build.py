@@ -80,6 +80,25 @@ def build_native(verbose: bool = False) -> str:
     return NATIVE_LIB
 
 
+def calls_in(obj: str) -> int:
+    """The call instructions in an object file's gfx950 code."""
+    import tempfile
+    tools = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin")
+
+    def run(tool, *args):
+        return subprocess.run([os.path.join(tools, tool), *args], capture_output=True, text=True, check=True).stdout
+
+    with tempfile.TemporaryDirectory() as d:
+        fat, code = os.path.join(d, "fat"), os.path.join(d, "code")
+        if ".hip_fatbin" not in run("llvm-objdump", "-h", obj):
+            return 0
+        run("llvm-objcopy", f"--dump-section=.hip_fatbin={fat}", obj, os.path.join(d, "rest"))
+        run("clang-offload-bundler", "--unbundle", "--type=o", f"--targets=hipv4-amdgcn-amd-amdhsa--{ARCH}",
+            f"--input={fat}", f"--output={code}")
+        asm = run("llvm-objdump", "-d", "--no-show-raw-insn", code)
+    return sum("s_swappc_b64" in line or "s_call_b64" in line for line in asm.splitlines())
+
+
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every source (in parallel, one object each) and link them into LIB_PATH
     (atomically replaced), then the `_native` module and the C example against it. Returns the library's path."""
@@ -97,6 +116,9 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         if proc.returncode != 0:
             sys.stderr.write(proc.stdout + proc.stderr)
             raise RuntimeError(f"hipcc failed on {src} with exit code {proc.returncode}")
+        calls = calls_in(obj)
+        if calls:  # moves between lanes and barriers are written for one body of code
+            raise RuntimeError(f"{src}: the compiler left {calls} calls in its kernels; mark the functions MSS_INLINED")
         return obj
 
     jobs = max(1, min(len(SOURCES), os.cpu_count() or 1, 16))

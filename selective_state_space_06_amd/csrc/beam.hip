@@ -157,10 +157,10 @@ __global__ __launch_bounds__(64 * kWaves) void beam_slices_kernel(SArgs a) {
         List list;
         float m = -INFINITY, s = 0.0f;  // of this lane's elements: the greatest, the sum of e^(v - m)
         Raw<E> raw[2] = {};
-        const auto load = [&](int64_t k, Raw<E>& r) {
+        const auto load = [&](int64_t k, Raw<E>& r) MSS_INLINED {
             load8<E, VEC>(p + k * kTile, a.V, clamp_tile(a.V - k * kTile), lane, r);
         };
-        const auto tile = [&](int64_t k, Raw<E>& r, auto first) {
+        const auto tile = [&](int64_t k, Raw<E>& r, auto first) MSS_INLINED {
             const int rem = clamp_tile(a.V - k * kTile);
             settle8<E, VEC>(a.V, rem, lane, r);
             float v[kE];
@@ -171,7 +171,7 @@ __global__ __launch_bounds__(64 * kWaves) void beam_slices_kernel(SArgs a) {
                 for (int e = 0; e < kE; ++e)
                     if (lane * kE + e >= rem) v[e] = -INFINITY;
             }
-            const auto sums = [&]() {
+            const auto sums = [&]() MSS_INLINED {
                 float best = v[0];
 #pragma unroll
                 for (int e = 1; e < kE; ++e) best = fmaxf(best, v[e]);
@@ -304,7 +304,7 @@ __global__ __launch_bounds__(64 * kMergeWaves) void beam_merge_kernel(SArgs a) {
             const bool over = done[n];
             int at = 0, token = 0;
             uint64_t order = 0;
-            const auto next = [&]() {
+            const auto next = [&]() MSS_INLINED {
                 order = 0;
                 if (over) {  // one continuation
                     if (at == 0) order = order64_of(scores[n]);

@@ -53,7 +53,7 @@ __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int64_t items = a.R * a.S;
     // One row's segment; adds the wave's dw_0 .. dw_{K-1}, dbias to s.
-    const auto pass = [&](int64_t row, int seg, float* s) {
+    const auto pass = [&](int64_t row, int seg, float* s) MSS_INLINED {
         const int64_t first = seg * a.seg_tiles;
         const int64_t end = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
         const int64_t ch = row % a.Dn, base = row * a.L;
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_
         Raw<E> nx, nd;
         S nh = 0;  // lane j: input j of the K - 1 before the tile, as it lies in memory (converted here, each load was
                    // waited for: 65 us)
-        const auto load = [&](int64_t k, auto whole) {
+        const auto load = [&](int64_t k, auto whole) MSS_INLINED {
             const int rem = decltype(whole)::value ? kTile : clamp_tile(a.L - k * kTile);
             load8<E, VEC>(xr + k * kTile, a.L, rem, lane, nx);
             load8<E, VEC>(static_cast<const S*>(a.dout) + base + k * kTile, a.L, rem, lane, nd);
@@ -91,6 +91,8 @@ __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_
                 nh = h ? h[lane < K - 1 ? lane : 0] : 0;
             }
         };
+        // Not MSS_INLINED, which would spill (aligned bf16 rows, K = 4: 19 registers); the build checks that no call is
+        // left.
         // WHOLE: the tile lies inside the row.  Rows that are no whole vectors have code of their own for such tiles (8 x
         // 1536 x 2047 f32: 60.5 us, 65 without; aligned bf16 rows would spill at five waves: 55 us for 50).
         const auto tile = [&](int64_t k, auto whole) {

@@ -205,7 +205,7 @@ __global__ __launch_bounds__(Place<W>::kThreads) void gated_fwd_kernel(GArgs a) 
         const auto x_ = static_cast<const S*>(a.x) + row * a.L, f_ = static_cast<const S*>(a.f) + row * a.L;
         const auto i_ = static_cast<const S*>(a.i) + row * a.L;
         Raw<E> nx{}, nf{}, ni{};  // the next tile's inputs, on their way while this one is computed
-        const auto load = [&](int64_t k) {
+        const auto load = [&](int64_t k) MSS_INLINED {
             const int64_t t = k * kTile;
             const int rem = clamp_tile(len - t);  // nothing past the sequence's end is read...
             if (rem > 0) {
@@ -217,7 +217,7 @@ __global__ __launch_bounds__(Place<W>::kThreads) void gated_fwd_kernel(GArgs a) 
         };
         load(first + at.wave);
         // A round of W tiles from tile k0.  FAST: every step of it lies inside the sequence, and w.small.
-        const auto round = [&](int64_t k0, auto fast) {
+        const auto round = [&](int64_t k0, auto fast) MSS_INLINED {
             constexpr bool FAST = decltype(fast)::value;
             const int64_t k = k0 + at.wave, t = k * kTile;
             const int on = FAST ? kTile : k < end ? clamp_tile(len - t) : 0;  // this tile's steps in the sequence
@@ -285,7 +285,7 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
     __shared__ float sums[W == 1 ? 4 : W];
     const Place<W> at;
     // One row's segment; returns this wave's share of its part of drate.
-    const auto pass = [&](int64_t row, int seg) {
+    const auto pass = [&](int64_t row, int seg) MSS_INLINED {
         const int64_t first = seg * a.seg_tiles;
         const int64_t end = first + a.seg_tiles < a.tiles ? first + a.seg_tiles : a.tiles;
         const int64_t len = length_of(a, row);
@@ -297,6 +297,8 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
             scan_up(P, H);
             g = fmaf(lane_of(P, 63), g, lane_of(H, 63));
         }
+        // Not MSS_INLINED, which is inlined before it is simplified and then spills (rows that are no whole vectors, one
+        // wave: 20 registers in f32); each form has one call site, and the build checks that no call is left.
         const auto round = [&](int64_t k0, auto fast) {
             constexpr bool FAST = decltype(fast)::value;
             const int64_t k = k0 + at.wave, t = k * kTile, p0 = row * a.L + t;
@@ -404,7 +406,7 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
         return FOLD ? 0.0f : wave_sum(drate);
     };
     // the waves' parts added in order, for the wave that leads `ways` of them
-    const auto total = [&](int wave, int ways, float part) {
+    const auto total = [&](int wave, int ways, float part) MSS_INLINED {
         if (ways == 1) return part;
         if (at.lane == 0) sums[wave] = part;
         __syncthreads();

@@ -6,6 +6,11 @@
 
 namespace mss {
 
+// For a kernel's lambdas: they move values between lanes and meet at barriers, which must not end up behind a call
+// (the gated scan's backward walk, which the compiler outlined when it had a second call site, gave wrong
+// results).  The build refuses kernels with calls.
+#define MSS_INLINED __attribute__((always_inline))
+
 // Values as types, for lambdas that are built twice.
 struct True { static constexpr bool value = true; };
 struct False { static constexpr bool value = false; };

@@ -1,0 +1,52 @@
+"""The build's own checks: kernels are one body of code, without calls."""
+import os
+import re
+import subprocess
+from concurrent.futures import ThreadPoolExecutor
+
+import pytest
+
+from selective_state_space_06_amd import build as b
+
+
+def compiled(src, out, *extra):
+    subprocess.run([b.hipcc(), *b.compile_flags(), *extra, "-o", str(out), str(src)], check=True, capture_output=True)
+    return str(out)
+
+
+def test_calls_are_counted(tmp_path):
+    text = """#include <hip/hip_runtime.h>
+    __device__ float OTHER f(float v) { return v * v + 1.0f; }
+    __global__ void k(float* p) { p[threadIdx.x] = f(p[threadIdx.x]); }
+    """
+    for how, calls in (("__attribute__((noinline))", 1), ("__attribute__((always_inline))", 0)):
+        src = tmp_path / f"k{calls}.hip"
+        src.write_text(text.replace("OTHER", how))
+        assert b.calls_in(compiled(src, tmp_path / f"k{calls}.o", "-c")) == calls
+    host = tmp_path / "h.hip"
+    host.write_text("int h() { return 1; }\n")
+    assert b.calls_in(compiled(host, tmp_path / "h.o", "-c")) == 0
+
+
+def test_built_objects_have_none():
+    objs = [os.path.join(b.PKG_DIR, "_build", os.path.splitext(s)[0] + ".o") for s in b.SOURCES]
+    if not all(map(os.path.exists, objs)):
+        pytest.skip("not built here")
+    assert [b.calls_in(o) for o in objs] == [0] * len(objs)
+
+
+def test_lambdas_with_lane_moves_are_inlined_whatever_the_compiler_thinks(tmp_path):
+    """Compiled with the compiler's own inlining off, only the two forms of the backward walks' inner lambdas
+    (for whole tiles and others) are functions of their own."""
+    def lambdas(name):
+        out = compiled(os.path.join(b.CSRC, name + ".hip"), tmp_path / (name + ".s"), "-S", "--offload-device-only",
+                       "-fno-inline-functions")
+        with open(out) as f:
+            return {m for m in re.findall(r"^\s*\.type\s+(\S+),@function", f.read(), re.M) if re.search(r"clE|clI", m)}
+
+    with ThreadPoolExecutor(3) as ex:
+        gated, conv, beam = ex.map(lambdas, ("gated_scan", "conv1d_bwd", "beam"))
+    assert not beam
+    for found, kernel in ((gated, "gated_bwd_kernel"), (conv, "conv_bwd_kernel")):
+        for m in found:
+            assert kernel in m and re.search(r"clINS_(True|False|4TrueE|5FalseE)", m), m
