@@ -62,6 +62,11 @@ NATIVE_SRC = os.path.join(CSRC, "native_calls.c")
 NATIVE_LIB = os.path.join(PKG_DIR, "_native.so")
 
 
+def have_python_headers() -> bool:
+    import sysconfig
+    return os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def build_native(verbose: bool = False) -> str:
     """Compile the CPython module `_native` (host code only) against the built library, which it finds
     beside itself. Returns its path."""
@@ -80,10 +85,16 @@ def build_native(verbose: bool = False) -> str:
     return NATIVE_LIB
 
 
-def calls_in(obj: str) -> int:
-    """The call instructions in an object file's gfx950 code."""
+def calls_in(obj: str) -> int | None:
+    """The call instructions in an object file's gfx950 code (None: the compiler came without the tools
+    that tell)."""
     import tempfile
-    tools = os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "llvm", "bin")
+    roots = (os.environ.get("ROCM_PATH"), os.path.dirname(os.path.dirname(hipcc())), "/opt/rocm")
+    dirs = [os.path.join(r, "llvm", "bin") for r in roots if r]
+    need = ("llvm-objdump", "llvm-objcopy", "clang-offload-bundler")
+    tools = next((d for d in dirs if all(os.path.exists(os.path.join(d, t)) for t in need)), None)
+    if tools is None:
+        return None
 
     def run(tool, *args):
         return subprocess.run([os.path.join(tools, tool), *args], capture_output=True, text=True, check=True).stdout
@@ -101,7 +112,8 @@ def calls_in(obj: str) -> int:
 
 def build(verbose: bool = False, extra: list[str] | None = None) -> str:
     """Compile every source (in parallel, one object each) and link them into LIB_PATH
-    (atomically replaced), then the `_native` module and the C example against it. Returns the library's path."""
+    (atomically replaced), then the C example and, where Python's headers are, the `_native` module
+    against it. Returns the library's path."""
     from concurrent.futures import ThreadPoolExecutor
 
     objdir = os.path.join(PKG_DIR, "_build")
@@ -133,8 +145,12 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         sys.stderr.write(proc.stdout + proc.stderr)
         raise RuntimeError(f"linking failed with exit code {proc.returncode}")
     os.replace(tmp, LIB_PATH)
-    build_native(verbose)
     build_example(verbose)
+    if have_python_headers():
+        build_native(verbose)
+    else:  # the library is whole without it; its absence is reported where it is used
+        sys.stderr.write("Python's headers are missing: _native, which the torch front end of the gated scan, the conv's "
+                         "gradients and beam search needs, is not built\n")
     return LIB_PATH
 
 

@@ -28,10 +28,36 @@ def test_calls_are_counted(tmp_path):
     assert b.calls_in(compiled(host, tmp_path / "h.o", "-c")) == 0
 
 
+def test_without_the_tools_nothing_is_said(tmp_path, monkeypatch):
+    there = os.path.exists
+    monkeypatch.setattr(os.path, "exists", lambda p: "llvm" not in str(p) and there(p))
+    assert b.calls_in(str(tmp_path / "any.o")) is None
+
+
+def test_the_library_builds_without_pythons_headers(tmp_path, monkeypatch, capsys):
+    """A user of the C library has no use for them; other errors of the module's build still end it."""
+    import sysconfig
+    paths, made = dict(sysconfig.get_paths(), include=str(tmp_path / "none")), []
+    monkeypatch.setattr(b, "SOURCES", ["abi.hip"])  # one small source stands for all; nothing in the tree is replaced
+    for name in ("PKG_DIR", "LIB_PATH", "NATIVE_LIB"):
+        monkeypatch.setattr(b, name, str(tmp_path / os.path.basename(getattr(b, name)) if name != "PKG_DIR" else tmp_path))
+    monkeypatch.setattr(b, "build_example", lambda verbose=False: made.append("example"))
+    monkeypatch.setattr(sysconfig, "get_paths", lambda *a, **k: paths)
+    native = b.LIB_PATH.replace(b.LIB_NAME, "_native.so")
+    assert b.build() == b.LIB_PATH and os.path.exists(b.LIB_PATH)
+    assert made == ["example"] and not os.path.exists(native)
+    assert "headers are missing" in capsys.readouterr().err
+    (tmp_path / "none").mkdir()
+    (tmp_path / "none" / "Python.h").write_text("#error no such thing\n")
+    with pytest.raises(RuntimeError, match="native_calls"):
+        b.build()
+
+
 def test_built_objects_have_none():
     objs = [os.path.join(b.PKG_DIR, "_build", os.path.splitext(s)[0] + ".o") for s in b.SOURCES]
     if not all(map(os.path.exists, objs)):
         pytest.skip("not built here")
+    assert b.calls_in(objs[0]) is not None
     assert [b.calls_in(o) for o in objs] == [0] * len(objs)
 
 
