@@ -276,12 +276,20 @@ def beam_select(logits, scores, finished=None, end_token=None, k=None, next_scor
     return got if next_finished is None else got + (next_finished,)
 
 
+def _state_tuple(states):
+    """The states as a tuple.  A tensor is refused: it would be taken for a sequence of its rows."""
+    import torch
+    if isinstance(states, torch.Tensor):
+        raise TypeError("states is a sequence of tensors, got one tensor")
+    return tuple(states)
+
+
 def beam_reorder(states, parents):
     """Every state (batch * beams, ...) in place: row b * beams + j becomes the row of beam
     parents[b, j] (mss_beam_reorder), on the current stream.  states: a sequence of float32, bfloat16 or
     int32 tensors (all layers' scan states and conv windows in one call); parents: (batch, beams) int32;
     a parent outside [0, beams) leaves its row as it is.  Returns states."""
-    given = tuple(states)
+    given = _state_tuple(states)
     _refuse_written(*given)
     _launch("beam_reorder", parents, given, parents)
     _note_written(*given)
@@ -414,7 +422,7 @@ class BeamSearchStep:
 
     def __init__(self, logits, scores, states, finished=None, end_token=None, stream=None):
         import torch
-        states = tuple(states)
+        states = _state_tuple(states)
         _refuse_written(scores, finished, *states)
         _same_device(logits, (scores, finished, *states))
         stream = _bound_stream(logits, stream)
