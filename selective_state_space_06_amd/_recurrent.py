@@ -382,14 +382,19 @@ def _make_conv():
 
 # ------------------------------------------------------------------------------------- bound steps
 
-def _empty_on(stream, shape, dtype, device):
+def _empty_on(stream, shape, dtype, device, fill=None):
     """Memory whose earlier users are ordered before work on `stream` (a raw handle)."""
     import torch
+
+    def make():
+        return torch.empty(shape, dtype=dtype, device=device) if fill is None else \
+            torch.full(shape, fill, dtype=dtype, device=device)
+
     with torch.cuda.device(device):
         if stream == torch.cuda.current_stream(device).cuda_stream:
-            return torch.empty(shape, dtype=dtype, device=device)
+            return make()
         with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-            return torch.empty(shape, dtype=dtype, device=device)
+            return make()
 
 
 class GatedUpdateStep:
@@ -417,7 +422,8 @@ class BeamSearchStep:
     """One step of a beam search bound to fixed device buffers: mss_beam_select on `logits` with
     `scores` (and `finished`) updated in place, then mss_beam_reorder of `states` by the parents it
     chose.  Arguments as for beam_select and beam_reorder; calling it returns (parents, tokens), its own
-    (batch, beams) int32 buffers, which the next call overwrites.  Without `finished` a beam that takes
+    (batch, beams) int32 buffers, which the next call overwrites.  States that cannot be reordered, or that
+    overlap logits, scores or finished, are refused here.  Without `finished` a beam that takes
     end_token goes on like any other."""
 
     def __init__(self, logits, scores, states, finished=None, end_token=None, stream=None):
@@ -426,7 +432,7 @@ class BeamSearchStep:
         _refuse_written(scores, finished, *states)
         _same_device(logits, (scores, finished, *states))
         stream = _bound_stream(logits, stream)
-        self.parents = _empty_on(stream, scores.shape, torch.int32, logits.device)
+        self.parents = _empty_on(stream, scores.shape, torch.int32, logits.device, fill=-1)
         self.tokens = _empty_on(stream, scores.shape, torch.int32, logits.device)
         floats = beam_select_scratch(*logits.shape, scores.shape[-1])
         scratch = _empty_on(stream, (floats,), torch.float32, logits.device)
@@ -438,6 +444,12 @@ class BeamSearchStep:
                              _ref(pa), _ref(to), _ref(fi), _ref(scr), stream)
         self._reorder_args = (_pointers(sts), len(sts), _ref(pa), stream)
         self._lib = load_library()
+        # What mss_beam_reorder refuses has to be refused before mss_beam_select has moved the scores: asked now, with
+        # parents of -1, which leave every row as it is.  What the selection reads or writes is no state either.
+        apart = [_desc(t.flatten(0, 1)) for t in (logits, scores, finished) if t is not None and t.ndim > 1]
+        with torch.cuda.device(logits.device):
+            st = self._lib.mss_beam_reorder(_pointers(sts + apart), len(sts) + len(apart), _ref(pa), stream)
+        _raise(st, "mss_beam_reorder")
 
     def __call__(self):
         _raise(self._lib.mss_beam_select(*self._select_args), "mss_beam_select")
