@@ -334,23 +334,33 @@ def _stream_of(dev_):
     return None
 
 
+_autograd = None
+
+
+def _autograd_calls():
+    """torch's (is_grad_enabled, increment_version), looked up once."""
+    global _autograd
+    if _autograd is None:
+        import torch
+        _autograd = torch.is_grad_enabled, torch.autograd.graph.increment_version
+    return _autograd
+
+
 def _refuse_written(*tensors):
     """Refuses tensors (None: none given) that a call is about to write and that autograd would have to
     differentiate through, as torch's own in-place operations refuse leaves."""
-    import torch
-    if torch.is_grad_enabled():
+    if _autograd_calls()[0]():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise ValueError("libmamba_scan writes this tensor in place, which has no gradient: pass a detached "
                                  "copy, or call under torch.no_grad()")
 
 
-def _note_written(*tensors):
-    """Raises the versions of tensors (None: none given) that a call has written through their addresses,
-    so that a backward that saved one of them raises instead of reading the new values.  (Tensors made under
-    inference_mode have no version, and are passed over.)"""
-    import torch
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+def _note_written(tensors):
+    """Raises the versions of tensors that a call has written through their addresses, so that a backward that
+    saved one of them raises instead of reading the new values.  (Tensors made under inference_mode have no
+    version, and are passed over.)"""
+    _autograd_calls()[1](tensors)
 
 
 def selective_scan_fwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, delta_softplus=True,
@@ -419,7 +429,8 @@ def causal_conv1d_update(state, x, weight, bias=None, silu=True, out=None):
     """One token of the conv per row; `state` (batch, d_inner, K - 1) in x's dtype is updated in
     place.  x: (batch, d_inner).  Returns out (batch, d_inner)."""
     import torch
-    _refuse_written(state, out)
+    written = (state,) if out is None else (state, out)
+    _refuse_written(*written)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     stream = _stream_of(x.device)
@@ -433,7 +444,7 @@ def causal_conv1d_update(state, x, weight, bias=None, silu=True, out=None):
                                    1 if silu else 0, _desc(out), stream)
     if st != 0:
         raise MssError(st, "mss_causal_conv1d_update")
-    _note_written(state, out)
+    _note_written(written)
     return out
 
 
@@ -691,7 +702,7 @@ class Conv1dUpdateStep:
         st = self._fn(*self._args)
         if st != 0:
             raise MssError(st, "mss_causal_conv1d_update")
-        _note_written(self._keep[0], self.out)
+        _note_written((self._keep[0], self.out))
         return self.out
 
 

@@ -158,14 +158,14 @@ def gated_scan_fwd(x, fgate, igate, rate, initial_state=None, seq_lens=None, ret
     (batch,) int32 on the device (None: all L; outputs past a sequence's end are 0).  Returns out (dtype
     of x), or (out, last_state) with last_state (batch, d_inner) float32."""
     import torch
-    given = (out, last_state)
+    given = [t for t in (out, last_state) if t is not None]
     _refuse_written(*given)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if return_last_state and last_state is None:
         last_state = torch.empty(x.shape[:2], dtype=torch.float32, device=x.device)
     _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, out, last_state if return_last_state else None, None)
-    _note_written(*given)
+    _note_written(given)
     return (out, last_state) if return_last_state else out
 
 
@@ -175,7 +175,7 @@ def gated_scan_fwd_save(x, fgate, igate, rate, initial_state=None, seq_lens=None
     (batch, d_inner, ceil(L / 512)) float32, the state entering every 512th step.  Returns
     (out, last_state, saved_states)."""
     import torch
-    given = (out, last_state, saved_states)
+    given = [t for t in (out, last_state, saved_states) if t is not None]
     _refuse_written(*given)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -184,7 +184,7 @@ def gated_scan_fwd_save(x, fgate, igate, rate, initial_state=None, seq_lens=None
     if saved_states is None:
         saved_states = _saved_like(x)
     _gated_fwd(x, fgate, igate, rate, initial_state, seq_lens, out, last_state, saved_states)
-    _note_written(*given)
+    _note_written(given)
     return out, last_state, saved_states
 
 
@@ -214,11 +214,12 @@ def gated_state_update(state, x, fgate, igate, rate, out=None):
     (batch, d_inner) float32 is updated in place.  x, fgate, igate: (batch, d_inner) float32 or
     bfloat16.  Returns out (batch, d_inner) in x's dtype."""
     import torch
-    _refuse_written(state, out)
+    written = (state,) if out is None else (state, out)
+    _refuse_written(*written)
     if out is None:
         out = torch.empty_like(x)
     _launch("gated_state_update", x, state, x, fgate, igate, rate, out)
-    _note_written(state, out)
+    _note_written(written)
     return out
 
 
@@ -254,7 +255,7 @@ def beam_select(logits, scores, finished=None, end_token=None, k=None, next_scor
     float32, parents int32, tokens int32), each (batch, k), best first, and with `finished` given also
     next_finished int32.  next_scores=scores and next_finished=finished update those in place."""
     import torch
-    given = (next_scores, parents, tokens, next_finished)
+    given = [t for t in (next_scores, parents, tokens, next_finished) if t is not None]
     _refuse_written(*given)
     # outputs after the model of scores where they have its shape (empty_like takes half the time of empty)
     shape = (logits.shape[0], scores.shape[-1] if k is None else int(k))
@@ -271,7 +272,7 @@ def beam_select(logits, scores, finished=None, end_token=None, k=None, next_scor
     floats = beam_select_scratch(*logits.shape, shape[1]) if ok else 0
     _launch("beam_select", logits, logits, scores, finished, -1 if end_token is None else int(end_token), next_scores,
             parents, tokens, next_finished, _scratch(floats, logits.device))
-    _note_written(*given)
+    _note_written(given)
     got = (next_scores, parents, tokens)
     return got if next_finished is None else got + (next_finished,)
 
@@ -292,7 +293,7 @@ def beam_reorder(states, parents):
     given = _state_tuple(states)
     _refuse_written(*given)
     _launch("beam_reorder", parents, given, parents)
-    _note_written(*given)
+    _note_written(given)
     return states
 
 
@@ -414,7 +415,7 @@ class GatedUpdateStep:
 
     def __call__(self):
         _raise(self._fn(*self._args), "mss_gated_state_update")
-        _note_written(self._keep[0], self.out)
+        _note_written((self._keep[0], self.out))
         return self.out
 
 
@@ -437,7 +438,7 @@ class BeamSearchStep:
         floats = beam_select_scratch(*logits.shape, scores.shape[-1])
         scratch = _empty_on(stream, (floats,), torch.float32, logits.device)
         self._keep = (logits, scores, finished, self.parents, self.tokens, scratch, *states)
-        self._written = (scores, finished, self.parents, self.tokens, *states)
+        self._written = [t for t in (scores, finished, self.parents, self.tokens, *states) if t is not None]
         lo, sc, fi, pa, to, scr, *sts = [_desc(t) for t in self._keep]
         self._descs = (lo, sc, fi, pa, to, scr, sts)
         self._select_args = (_ref(lo), _ref(sc), _ref(fi), -1 if end_token is None else int(end_token), _ref(sc),
@@ -454,5 +455,5 @@ class BeamSearchStep:
     def __call__(self):
         _raise(self._lib.mss_beam_select(*self._select_args), "mss_beam_select")
         _raise(self._lib.mss_beam_reorder(*self._reorder_args), "mss_beam_reorder")
-        _note_written(*self._written)
+        _note_written(self._written)
         return self.parents, self.tokens
