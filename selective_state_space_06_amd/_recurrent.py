@@ -108,6 +108,20 @@ def _native():
     return _native_module
 
 
+_raw_stream_of = None
+
+
+def _raw_stream():
+    """The function from a device index to its current stream's handle: torch's own without the Stream object
+    (1 us less a call), which is private to torch and may be absent."""
+    global _raw_stream_of
+    if _raw_stream_of is None:
+        import torch
+        _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream_of
+
+
 def _launch(name, x, *args):
     """The native call `name` on the current stream of x's device."""
     import torch
@@ -115,7 +129,7 @@ def _launch(name, x, *args):
     index = x.get_device()
     if index < 0:
         raise ValueError("libmamba_scan takes device tensors")
-    stream = torch._C._cuda_getCurrentRawStream(index)  # current_stream() without its object: 1 us less
+    stream = _raw_stream()(index)
     if index == torch.cuda.current_device():
         st = fn(*args, stream)
     else:

@@ -15,3 +15,13 @@ def test_a_single_tensor_is_no_sequence_of_states():
         mss.BeamSearchStep(torch.zeros(2, 2, 5), torch.zeros(2, 2), square)
     with pytest.raises(ValueError, match="device tensors"):  # the sequence is looked into
         mss.beam_reorder([square], parents)
+
+
+def test_streams_without_torchs_private_call(monkeypatch):
+    import torch
+
+    from selective_state_space_06_amd import _recurrent
+    monkeypatch.setattr(_recurrent, "_raw_stream_of", None)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: type("S", (), {"cuda_stream": 40 + index}))
+    assert _recurrent._raw_stream()(2) == 42
