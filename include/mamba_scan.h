@@ -429,7 +429,7 @@ int mss_gated_scan_fwd(const mss_tensor_t* x, const mss_tensor_t* fgate, const m
  *                        with out and last_state NULL writes it alone)
  *   dout                 (batch, d_inner, L)  dtype of x
  *   dx, dfgate, digate   (batch, d_inner, L)  dtype of x, written (0 past a sequence's end)
- *   drate                (d_inner,)           f32, written (sum over batch and time, fixed order)
+ *   drate                (d_inner,)           f32, written (sum over batch and time in fp32, fixed order)
  *   dinitial_state       (batch, d_inner)     f32, nullable, written
  * A NaN reaches the gradients whose formula it stands in.  At a closed gate (fgate -inf) dx, dfgate and
  * digate are 0 for |x| up to 1e19.
@@ -457,7 +457,7 @@ int mss_gated_state_update(const mss_tensor_t* state, const mss_tensor_t* x, con
  *   dout            (batch, d_inner, L)      dtype of x
  *   dfinal_state    (batch, d_inner, K - 1)  dtype of x, nullable
  *   dx              (batch, d_inner, L)      dtype of x, written
- *   dweight         (d_inner, K)             f32, written (sum over batch and time, fixed order)
+ *   dweight         (d_inner, K)             f32, written (sum over batch and time in fp32, fixed order)
  *   dbias           (d_inner,)               f32, nullable, written (also when bias is NULL)
  *   dinitial_state  (batch, d_inner, K - 1)  dtype of x, nullable, written (also when initial_state is
  *                                            NULL: the gradient at zeros)
@@ -476,7 +476,13 @@ int mss_causal_conv1d_bwd(const mss_tensor_t* x, const mss_tensor_t* weight, con
  * has one continuation, end_token, at scores[i] itself.  A continuation whose score is -inf or not a
  * number does not exist: masked logits (-inf), NaN logits (taken as -inf), a beam that was never used
  * (scores -inf), a row with a logit of +inf.  Higher scores come first; equal scores go by beam,
- * within a beam by logit, then by token.  Scores are formed and compared in 64 bits.
+ * within a beam by logit, then by token.  Scores are formed from score, logit and normaliser and compared
+ * in 64 bits.  The normaliser's exponentials and each lane's sum of them are fp32 (64 bits where lanes,
+ * waves and slices join): it is off by about 1e-7, at most by (6 ln vocab + vocab / 1024 + 32) 2^-24.
+ * Candidates of different beams that stand closer than that are ordered by it, unless the beams' rows are
+ * copies, whose normalisers are the same to the bit; a beam's own candidates are not touched by it.
+ * next_scores is the score rounded to fp32: one below fp32's range is written as -inf, with its parent and
+ * token, and has no continuation in the step after.
  *   logits         (batch, beams, vocab)  f32 or bf16
  *   scores         (batch, beams)         f32
  *   finished       (batch, beams)         I32, nullable (no beam is); nonzero: at its end

@@ -5,9 +5,10 @@
 // a finished beam has one, its end token at its own score.  Per request the k best are kept.  A
 // beam's continuations are ordered by their logits alone, so one pass over the logits gives both a
 // slice's greatest logit and sum of exponentials and its k best (slices kernel); a second, small
-// kernel forms the slices' scores and merges a request's lists.  Scores are compared in 64 bits: they
-// differ by the beams' sums and normalisers, whose 32-bit rounding would decide between near
-// candidates.
+// kernel forms the slices' scores and merges a request's lists.  Scores are formed and compared in 64
+// bits, so that their own rounding (6e-7 at a score of -10) decides nothing; the normaliser in them is a sum of fp32
+// exponentials, kept in fp32 by each lane and joined in 64 bits (measured 1.4e-8 to 1e-7 off), and decides
+// between candidates of different beams that stand closer than that.
 //
 // Logits are compared as whole numbers of the same order (order_of), with the token behind them as one
 // 64-bit key (a higher value, then a lower token).  A wave keeps its k best as a list spread over its
@@ -135,8 +136,8 @@ __device__ __forceinline__ uint64_t merge_lists(const uint64_t* lists, int count
 }
 
 // One block per (row, slice of the vocabulary), its waves on successive parts of the slice, each with two
-// tiles on their way (64 x 8 x 128008 f32: 47 us, the card's read rate; one wave with one tile on its way and
-// a list of values and tokens apart 57).  VEC: rows are whole aligned 16-byte vectors.
+// tiles on their way (64 x 8 x 128008 f32: 47 to 54 us by the card, 4.8 to 5.6 TB/s; one wave with one tile on its way
+// and a list of values and tokens apart 57).  VEC: rows are whole aligned 16-byte vectors.
 constexpr int kWaves = 8;
 
 template <class E, bool VEC>
@@ -412,9 +413,13 @@ void reorder_u(RArgs& a, hipStream_t s) {
     else if constexpr (sizeof(U) < 16) reorder_n<U, 64, 1>(a, s);
 }
 
-// Slices per row: blocks for every CU twice over (64 x 8 x 128008 f32: 59 us; four times 68, eight times 64:
-// each wave fills a list of its own; four times with four waves a block 61), each wave with a tile, and
-// lists that fit the merging block's shared memory.
+// Slices per row: blocks for every CU twice over, each wave with a tile, and lists that fit the merging block's shared
+// memory.  More blocks mean more lists to fill, one a wave.  Microseconds a call with blocks for every CU
+//                                        twice   four times   eight times
+//   64 x 8 x 128008 f32                   58.0       67.8         64.4
+//   64 x 8 x 128007 f32, 1/4 finished     51.5       61.4         59.0
+//   64 x 8 x 128008 bf16                  49.2       52.4         57.9
+//   32 x 16 x 32000 bf16                  35.3       43.0         49.0
 constexpr int64_t kMergeBytes = 56 << 10;
 void plan_select(int64_t rows, int64_t N, int64_t V, int64_t K, int64_t* per, int* slices) {
     const int64_t tiles = (V + kTile - 1) / kTile;
