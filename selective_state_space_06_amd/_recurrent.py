@@ -327,8 +327,9 @@ class GatedScanFunction:
     initial_state, seq_lens) -> (out, last_state), differentiable in x, fgate, igate, rate and
     initial_state (initial_state, seq_lens may be None).  The forward keeps one state in 512 for the
     backward.  Decoding goes on from last_state.detach().clone(): the calls that write a state in place
-    refuse one that requires gradients.  To capture a training step in a graph, capture gated_scan_fwd_save and gated_scan_bwd:
-    autograd ends the process when it captures a backward of leaves that an eager graph still holds."""
+    refuse one that requires gradients.  To capture a training step in a graph, capture
+    gated_scan_fwd_save and gated_scan_bwd (tested); a captured backward() of this wrapper is untested.
+    First derivatives in reverse mode only: no double backward, no forward mode, no vmap."""
 
     @staticmethod
     def apply(x, fgate, igate, rate, initial_state=None, seq_lens=None):

@@ -12,7 +12,8 @@
 // y needs the last K - 1 inputs of the lane before (a whole-wave shift; those before the tile
 // are loaded with it), dx the first K - 1 dy of the lane after; the first lane's dy is kept for the tile that
 // precedes it in time.  A tile's loads are issued before the one after it in time is computed.  The
-// sums over time stay in registers.
+// sums over time stay in registers, in fp32 (8 x 1536 x 2047 f32: all gradients together are
+// 1.5e-7 off, 0.8e-7 with 64-bit sums).
 #include "device_math.hpp"
 #include "mss_internal.hpp"
 #include "row_io.hpp"
@@ -37,14 +38,17 @@ struct CArgs {
     int S;                  // segments per row
 };
 
-// dy = dout silu'(y)
+// dy = dout silu'(y).  1 - s loses digits where s is near 1: up to u y = 6e-8 y, against a silu' of about 1 there.
 __device__ __forceinline__ float silu_grad(float y) {
     const float s = fast_rcp(1.0f + fast_exp2(-y * kLog2e));
     return s * fmaf(y, 1.0f - s, 1.0f);
 }
 
-// Five waves a SIMD for aligned bf16 rows (2.8B layer: 52.6 us, 54.5 at four); the others would spill (8 x
-// 1536 x 2047 f32: 58 us at four, 70 at five).
+// Five waves a SIMD for aligned bf16 rows (2.8B layer with silu: 52.6 us, 54.5 at four); the other rows' kernels would
+// spill (8 x 1536 x 2047 f32: 58 us at four, 70 at five).  Of the aligned ones K = 4 without silu does spill at
+// five, 13 registers in 36 bytes a lane: 35.8 MB more are written on the 2.8B layer and the call takes 53.5 us where
+// silu's takes 48.8.  Rows that are no whole vectors spill 119 (bf16) and 138 (f32) scalar registers to lanes of
+// vector ones: the row's walk is inlined twice, for parts and for whole channels.
 template <class E, int K, bool SILU, bool VEC>
 __global__ __launch_bounds__(256, VEC && E::kPerVec == 8 ? 5 : 4) void conv_bwd_kernel(CArgs a) {
     using S = typename E::storage;

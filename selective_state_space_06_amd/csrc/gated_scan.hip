@@ -50,8 +50,8 @@ struct GArgs {
 
 // ---- gates
 // q = 1 - a^2 = 1 - e^-y, y = 2 s, formed as such loses its digits as y -> 0 (a decay of 0.99 leaves
-// five), so up to y = 1/2 it is y (k0 + .. + k4 y^4), the minimax fit of (1 - e^-y) / y there (relative
-// error 7.7e-8, 1.9e-7 with fp32's rounding).
+// five), so up to y = 1/2 it is y (k0 + .. + k4 y^4), a fit of (1 - e^-y) / y there (relative error up to 1.04e-7, at
+// y = 1/2; with fp32's rounding 2.0e-7, and 2.3e-7 in the form by r below).
 constexpr float kQ[5] = {0.9999999403953552f, -0.4999924898147583f, 0.16654814779758453f, -0.04100127890706062f,
                          0.006771037820726633f};
 
@@ -324,7 +324,9 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
                 }
             }
             // of every step: a, r, s (1 - r), a^2 p x / m, p m, x (1 - p), p m x, dout: no more of them than the
-            // second pass needs, so that four waves share a SIMD (2.8B layer bf16: 115 us, 120 at three)
+            // second pass needs, so that four waves share a SIMD (2.8B layer bf16: 115 us, 120 at three).  bf16 rows
+            // with one wave spill two registers all the same (12 bytes a lane; 4% more is written on that layer):
+            // the loop over the batch around the walk takes them.
             float av[kE], rv[kE], sc[kE], into[kE], pm[kE], xc[kE], v[kE], d[kE];
             float P = 1.0f, H = 0.0f, V = 0.0f;
             rf.unpack(rv);
@@ -440,7 +442,7 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
 }
 
 // drate[d] = sum over the rows of channel d and their segments: a wave per channel, each lane every 64th
-// part in order, then the lanes.
+// part in order, then the lanes.  All of drate's sums are fp32: over time a lane's at most L / 64 terms in a row.
 __global__ __launch_bounds__(256) void gated_rate_kernel(const float* part, float* drate, int64_t Dn, int64_t Bt, int S) {
     const int lane = threadIdx.x & 63;
     for (int64_t d = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); d < Dn; d += (int64_t)gridDim.x * 4) {
@@ -493,6 +495,13 @@ struct Plan {
 //    1536 x 131072 bf16    370 / 632     368 / 588     315 / 563
 //     512 x 32768 f32     82.3 / 201    52.1 / 98.9   49.9 / 96.5
 //      64 x 131072 f32     296 / 488    93.2 / 169    95.1 / 137    four, eight segments: 42.7 / 58.4
+// Up to 1024 rows any second tile brings four waves, for the few rows' sake; near 1024 rows, and where the rows of a
+// channel then go by parts, one wave is as fast or faster in the backward (kernels alone):
+//      64 x   3584 bf16    8.6 / 10.7    4.6 / 6.3
+//     512 x   1024 f32     4.5 / 7.4     4.5 / 6.8
+//    1024 x   1536 f32     7.3 / 11.8    7.7 / 12.2
+//    1024 x   3584 bf16   10.0 / 14.8   10.0 / 18.2
+//    1024 x   1024 bf16    4.4 / 6.7     6.0 / 11.7
 Plan plan_of(int64_t R, int64_t L, bool bf16, bool vec) {
     Plan p;
     p.tiles = (L + kTile - 1) / kTile;
