@@ -325,8 +325,8 @@ __global__ __launch_bounds__(Place<W>::kThreads, W == 1 || VEC ? 4 : 3) void gat
             }
             // of every step: a, r, s (1 - r), a^2 p x / m, p m, x (1 - p), p m x, dout: no more of them than the
             // second pass needs, so that four waves share a SIMD (2.8B layer bf16: 115 us, 120 at three).  bf16 rows
-            // with one wave spill two registers all the same (12 bytes a lane; 4% more is written on that layer):
-            // the loop over the batch around the walk takes them.
+            // with one wave spill two registers all the same (12 bytes a lane; 4% more is written on that layer;
+            // aligned rows compiled without the loop over the batch around the walk spill none).
             float av[kE], rv[kE], sc[kE], into[kE], pm[kE], xc[kE], v[kE], d[kE];
             float P = 1.0f, H = 0.0f, V = 0.0f;
             rf.unpack(rv);
