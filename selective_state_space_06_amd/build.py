@@ -87,7 +87,7 @@ def build_native(verbose: bool = False) -> str:
 
 def calls_in(obj: str) -> int | None:
     """The call instructions in an object file's gfx950 code (None: the compiler came without the tools
-    that tell)."""
+    that tell, or with others)."""
     import tempfile
     roots = (os.environ.get("ROCM_PATH"), os.path.dirname(os.path.dirname(hipcc())), "/opt/rocm")
     dirs = [os.path.join(r, "llvm", "bin") for r in roots if r]
@@ -103,10 +103,13 @@ def calls_in(obj: str) -> int | None:
         fat, code = os.path.join(d, "fat"), os.path.join(d, "code")
         if ".hip_fatbin" not in run("llvm-objdump", "-h", obj):
             return 0
-        run("llvm-objcopy", f"--dump-section=.hip_fatbin={fat}", obj, os.path.join(d, "rest"))
-        run("clang-offload-bundler", "--unbundle", "--type=o", f"--targets=hipv4-amdgcn-amd-amdhsa--{ARCH}",
-            f"--input={fat}", f"--output={code}")
-        asm = run("llvm-objdump", "-d", "--no-show-raw-insn", code)
+        try:
+            run("llvm-objcopy", f"--dump-section=.hip_fatbin={fat}", obj, os.path.join(d, "rest"))
+            run("clang-offload-bundler", "--unbundle", "--type=o", f"--targets=hipv4-amdgcn-amd-amdhsa--{ARCH}",
+                f"--input={fat}", f"--output={code}")
+            asm = run("llvm-objdump", "-d", "--no-show-raw-insn", code)
+        except subprocess.CalledProcessError:
+            return None
     return sum("s_swappc_b64" in line or "s_call_b64" in line for line in asm.splitlines())
 
 

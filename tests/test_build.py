@@ -34,6 +34,14 @@ def test_without_the_tools_nothing_is_said(tmp_path, monkeypatch):
     assert b.calls_in(str(tmp_path / "any.o")) is None
 
 
+def test_tools_that_refuse_end_no_build(tmp_path, monkeypatch):
+    src = tmp_path / "k.hip"
+    src.write_text("#include <hip/hip_runtime.h>\n__global__ void k(float* p) { p[0] = 1.0f; }\n")
+    obj = compiled(src, tmp_path / "k.o", "-c")
+    monkeypatch.setattr(b, "ARCH", "gfx90a")  # no such code in the object
+    assert b.calls_in(obj) is None
+
+
 def test_the_library_builds_without_pythons_headers(tmp_path, monkeypatch, capsys):
     """A user of the C library has no use for them; other errors of the module's build still end it."""
     import sysconfig
