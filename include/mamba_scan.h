@@ -395,7 +395,7 @@ int mss_ssd_scan_fwd(const mss_tensor_t* x, const mss_tensor_t* dt, const mss_te
  *     h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(igate_t) x_t,    out_t = h_t
  * (the input's weight sqrt(1 - a^2) keeps the state's size as the decay changes).
  *   x, fgate, igate  (batch, d_inner, L)   f32 or bf16, one dtype
- *   rate             (d_inner,)            f32, positive and finite (0 holds the state and lets nothing
+ *   rate             (d_inner,)            f32, positive, at most 1e38 (0 holds the state and lets nothing
  *                                          in; the gradient to rate is taken as 0 through sqrt there; a
  *                                          negative or infinite rate has no meaning: its channel's
  *                                          results may be NaN)
