@@ -49,9 +49,10 @@
 extern "C" {
 #endif
 
-#define MSS_VERSION 20100 /* major * 10000 + minor * 100 + patch */
+#define MSS_VERSION 20200 /* major * 10000 + minor * 100 + patch */
 
-typedef enum { MSS_F32 = 0, MSS_BF16 = 1, MSS_I32 = 2 } mss_dtype_t;  /* I32: lengths, beams, tokens */
+/* I32: lengths, beams, tokens.  F8E4M3: the 8-bit type without infinities (greatest value 448), an output alone */
+typedef enum { MSS_F32 = 0, MSS_BF16 = 1, MSS_I32 = 2, MSS_F8E4M3 = 3 } mss_dtype_t;
 
 typedef enum {
     MSS_OK = 0,
@@ -510,6 +511,135 @@ int mss_beam_select(const mss_tensor_t* logits, const mss_tensor_t* scores, cons
  *   parents  (batch, beams)  I32, beams at most 64 (MSS_ERR_UNSUPPORTED)
  */
 int mss_beam_reorder(const mss_tensor_t* const* states, int count, const mss_tensor_t* parents, void* stream);
+
+/*
+ * ---- RMS norm, linear attention with a decay per head, token log probabilities.  The rules of the section before:
+ * scratch is the caller's, every call can be captured with no call before, and gives the same bits on every run.
+ *
+ * RMS norm with the residual stream's addition, the step in front of a layer.  Per row of width W:
+ *     z = x + residual  (rounded to the stream's type: what residual_out holds and the norm is of; x without residual)
+ *     rstd = 1 / sqrt(mean(z^2) + eps),   out = z rstd weight
+ * and in 8 bits (out of MSS_F8E4M3) out = (z rstd weight) / scale rounded to nearest even, with
+ * scale = max(max |z rstd weight|, 2^-100) / 448 over the row, or over each 128 columns of it: out scale is the value.
+ *   x             (..., W)   f32 or bf16, 2 to 4 dimensions
+ *   residual      (..., W)   f32 or bf16, nullable
+ *   weight        (W,)       f32
+ *   eps           not negative
+ *   out           (..., W)   dtype of x, or MSS_F8E4M3 with scales, written
+ *   residual_out  (..., W)   dtype of residual, written; given with residual alone; may be residual (in place)
+ *   rstd          (...)      f32, nullable, written: for the backward
+ *   scales        (..., 1) or (..., ceil(W / 128))   f32, written; given with an 8-bit out alone
+ * W is at most 16384 (MSS_ERR_UNSUPPORTED above).  No other overlap of an output.  Sums are fp32: a row with
+ * |z| above 1e18 may overflow its sum of squares, and then gives 0.  A NaN, or an infinity, in a row makes its outputs
+ * NaN, or 0 beside the infinity.
+ */
+int mss_rms_norm_fwd(const mss_tensor_t* x, const mss_tensor_t* residual, const mss_tensor_t* weight, float eps,
+                     const mss_tensor_t* out, const mss_tensor_t* residual_out, const mss_tensor_t* rstd,
+                     const mss_tensor_t* scales, void* stream);
+
+/*
+ * Gradients of the RMS norm given dout = dL/dout and dresidual_out = dL/d residual_out (nullable: 0).
+ *   z              (..., W)   the forward's residual_out, or its x without residual
+ *   weight, rstd   as passed to, and written by, the forward
+ *   dout           (..., W)   dtype of x
+ *   dresidual_out  (..., W)   dtype of z, nullable
+ *   dx             (..., W)   dtype of dout, written: dL/dz
+ *   dresidual      (..., W)   dtype of z, nullable, written: dL/dz too (where z has dout's type, dx is both)
+ *   dweight        (W,)       f32, nullable, written (sum over rows in fp32, fixed order); scratch with it alone
+ * No output may overlap an input or another output.
+ */
+int mss_rms_norm_bwd_scratch(int64_t rows, int64_t width, int64_t* floats);
+int mss_rms_norm_bwd(const mss_tensor_t* z, const mss_tensor_t* weight, const mss_tensor_t* rstd,
+                     const mss_tensor_t* dout, const mss_tensor_t* dresidual_out, const mss_tensor_t* dx,
+                     const mss_tensor_t* dresidual, const mss_tensor_t* dweight, const mss_tensor_t* scratch,
+                     void* stream);
+
+/*
+ * Linear attention with one constant decay per head.  For every batch b and head h, with a = exp(-rate[h]):
+ *     S_t = a S_{t-1} + k_t v_t^T   (key_dim x value_dim),    out_t = scale S_t^T q_t
+ *   q              (batch, L, q_heads, key_dim)     f32 or bf16
+ *   k              (batch, L, k_heads, key_dim)     dtype of q
+ *   v              (batch, L, v_heads, value_dim)   dtype of q
+ *   rate           (heads,)                         f32, not negative (0: no decay; infinite: each step sees itself
+ *                                                   alone; a NaN or negative rate has no meaning)
+ *   initial_state  (batch, heads, key_dim, value_dim) f32, nullable (zeros)
+ *   seq_lens       (batch,)                         I32 in device memory, nullable (all L), clamped to [0, L] on the
+ *                                                   device: past a sequence's end the state is held and out is 0,
+ *                                                   whatever the inputs hold there
+ *   out            (batch, L, heads, value_dim)     dtype of q, written
+ *   last_state     (batch, heads, key_dim, value_dim) f32, nullable, written
+ * q, k and v may have fewer heads than rate, of which each is shared by heads / q_heads (k_heads, v_heads) heads in a
+ * row; they must divide heads (MSS_ERR_SHAPE).  key_dim and value_dim are multiples of 16 up to 128
+ * (MSS_ERR_UNSUPPORTED otherwise).  All but rate and seq_lens are 16-byte aligned (MSS_ERR_LAYOUT).  No output may
+ * overlap an input or another output.
+ * Computed in chunks of 64 steps (f32: 32) on the matrix cores; the state is fp32.  bf16 inputs are taken as they are,
+ * states and scores to 2^-17, what enters the state to 2^-25; f32 inputs, whose size is below 3.38e38, in three bf16
+ * parts, products to 2^-24.  An infinity or a NaN in a chunk may reach all its outputs, those before it among them, and
+ * all later ones.
+ */
+int mss_linear_attention_scratch(int64_t batch, int64_t L, int64_t heads, int64_t q_heads, int64_t k_heads,
+                                 int64_t v_heads, int64_t key_dim, int64_t value_dim, int64_t* fwd_floats,
+                                 int64_t* bwd_floats);
+int mss_linear_attention_fwd(const mss_tensor_t* q, const mss_tensor_t* k, const mss_tensor_t* v,
+                             const mss_tensor_t* rate, float scale, const mss_tensor_t* initial_state,
+                             const mss_tensor_t* seq_lens, const mss_tensor_t* out, const mss_tensor_t* last_state,
+                             const mss_tensor_t* scratch, void* stream);
+
+/*
+ * Gradients of linear attention given dout = dL/dout and dlast_state = dL/d last_state (nullable: 0).  The decay is a
+ * constant of the layer: it has no gradient here.
+ *   q, k, v, rate, scale, initial_state, seq_lens   as passed to the forward
+ *   dout            (batch, L, heads, value_dim)   dtype of q
+ *   dq, dk, dv      the shapes and dtype of q, k, v, written (0 past a sequence's end); a head that several share has
+ *                   the sum over them, in fp32 and in their order
+ *   dinitial_state  (batch, heads, key_dim, value_dim) f32, nullable, written (also when initial_state is NULL: the
+ *                   gradient at zeros)
+ */
+int mss_linear_attention_bwd(const mss_tensor_t* q, const mss_tensor_t* k, const mss_tensor_t* v,
+                             const mss_tensor_t* rate, float scale, const mss_tensor_t* initial_state,
+                             const mss_tensor_t* seq_lens, const mss_tensor_t* dout, const mss_tensor_t* dlast_state,
+                             const mss_tensor_t* dq, const mss_tensor_t* dk, const mss_tensor_t* dv,
+                             const mss_tensor_t* dinitial_state, const mss_tensor_t* scratch, void* stream);
+
+/*
+ * One token of linear attention: state (batch, heads, key_dim, value_dim) f32, 16-byte aligned, updated in place;
+ * q (batch, q_heads, key_dim), k (batch, k_heads, key_dim), v (batch, v_heads, value_dim) f32 or bf16; rate (heads,)
+ * f32; out (batch, heads, value_dim) dtype of q, written.  Sizes as above; arithmetic in fp32.  state and out may not
+ * overlap an input or each other.
+ */
+int mss_linear_attention_update(const mss_tensor_t* state, const mss_tensor_t* q, const mss_tensor_t* k,
+                                const mss_tensor_t* v, const mss_tensor_t* rate, float scale, const mss_tensor_t* out,
+                                void* stream);
+
+/*
+ * Log probabilities of given tokens under p = softmax(logits), each row's entropy and its most probable tokens.
+ *   logits        (..., vocab)  f32 or bf16, 2 to 4 dimensions
+ *   tokens        (...)         I32; one outside [0, vocab) is no token: its log probability is 0, without gradient
+ *   logprobs      (...)         f32, written: log p[token]
+ *   entropy       (...)         f32, nullable, written: -sum p log p
+ *   top_logprobs  (..., k)      f32, written: the k greatest log p, best first, equal ones by token
+ *   top_tokens    (..., k)      I32, written; both or neither; where a row has fewer logits that are not masked: -inf
+ *                               and -1
+ *   saved         (..., 3)      f32, nullable, written: for the backward
+ * A masked logit (-inf) has p = 0 and adds nothing.  A row of them alone has no token: its log probability is -inf
+ * (0 for no token), its entropy 0, its gradient 0.  A NaN or +inf logit makes the row's log probabilities and entropy
+ * NaN (0 for no token stays); a NaN is no alternative.  k is at most 64 (MSS_ERR_UNSUPPORTED).  No output may overlap an
+ * input or another output.
+ */
+int mss_token_logprobs_scratch(int64_t rows, int64_t vocab, int64_t k, int64_t* floats);
+int mss_token_logprobs_fwd(const mss_tensor_t* logits, const mss_tensor_t* tokens, const mss_tensor_t* logprobs,
+                           const mss_tensor_t* entropy, const mss_tensor_t* top_logprobs,
+                           const mss_tensor_t* top_tokens, const mss_tensor_t* saved, const mss_tensor_t* scratch,
+                           void* stream);
+
+/*
+ * The gradient to the logits given dlogprobs = dL/d logprobs (...) and dentropy = dL/d entropy (...) (f32; dentropy
+ * nullable: 0); saved as the forward wrote it for these logits; dlogits (..., vocab) dtype of logits, written, and may
+ * be logits (in place).  No other overlap of it.
+ */
+int mss_token_logprobs_bwd(const mss_tensor_t* logits, const mss_tensor_t* tokens, const mss_tensor_t* saved,
+                           const mss_tensor_t* dlogprobs, const mss_tensor_t* dentropy, const mss_tensor_t* dlogits,
+                           void* stream);
 
 /*
  * Frees every workspace buffer the library holds, on every device (current ones and those

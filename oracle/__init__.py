@@ -325,3 +325,11 @@ from .recurrent import (  # noqa: E402,F401
     gated_scan_bwd,
     gated_state_update,
 )
+from .layers import (  # noqa: E402,F401
+    linear_attention,
+    linear_attention_bwd,
+    rms_norm,
+    rms_norm_bwd,
+    token_logprobs,
+    token_logprobs_bwd,
+)

@@ -13,7 +13,7 @@ import threading
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG_DIR, "libmamba_scan.so")
 
-MSS_F32, MSS_BF16, MSS_I32 = 0, 1, 2
+MSS_F32, MSS_BF16, MSS_I32, MSS_F8E4M3 = 0, 1, 2, 3
 STATUS = {0: "MSS_OK", -1: "MSS_ERR_NULL_ARG", -2: "MSS_ERR_SHAPE", -3: "MSS_ERR_DTYPE",
           -4: "MSS_ERR_LAYOUT", -5: "MSS_ERR_ALIAS", -6: "MSS_ERR_UNSUPPORTED", -7: "MSS_ERR_HIP"}
 
@@ -27,6 +27,10 @@ EXPORTS = ("mss_selective_scan_fwd", "mss_selective_scan_fwd_with_state",
            "mss_gated_scan_scratch", "mss_gated_scan_fwd", "mss_gated_scan_bwd", "mss_gated_state_update",
            "mss_causal_conv1d_bwd_scratch", "mss_causal_conv1d_bwd",
            "mss_beam_select_scratch", "mss_beam_select", "mss_beam_reorder",
+           "mss_rms_norm_fwd", "mss_rms_norm_bwd_scratch", "mss_rms_norm_bwd",
+           "mss_linear_attention_scratch", "mss_linear_attention_fwd", "mss_linear_attention_bwd",
+           "mss_linear_attention_update",
+           "mss_token_logprobs_scratch", "mss_token_logprobs_fwd", "mss_token_logprobs_bwd",
            "mss_status_string", "mss_version")
 
 
@@ -144,6 +148,20 @@ def load_library(path: str = LIB_PATH):
             lib.mss_beam_select.argtypes = [_TP] * 3 + [ctypes.c_int] + [_TP] * 5 + [ctypes.c_void_p]
             lib.mss_beam_reorder.restype = ctypes.c_int
             lib.mss_beam_reorder.argtypes = [ctypes.POINTER(_TP), ctypes.c_int, _TP, ctypes.c_void_p]
+            f32 = ctypes.c_float
+            for name, args in {
+                    "rms_norm_fwd": [_TP] * 3 + [f32] + [_TP] * 4 + [ctypes.c_void_p],
+                    "rms_norm_bwd_scratch": [i64, i64, i64p],
+                    "rms_norm_bwd": [_TP] * 9 + [ctypes.c_void_p],
+                    "linear_attention_scratch": [i64] * 8 + [i64p, i64p],
+                    "linear_attention_fwd": [_TP] * 4 + [f32] + [_TP] * 5 + [ctypes.c_void_p],
+                    "linear_attention_bwd": [_TP] * 4 + [f32] + [_TP] * 9 + [ctypes.c_void_p],
+                    "linear_attention_update": [_TP] * 5 + [f32, _TP, ctypes.c_void_p],
+                    "token_logprobs_scratch": [i64, i64, i64, i64p],
+                    "token_logprobs_fwd": [_TP] * 8 + [ctypes.c_void_p],
+                    "token_logprobs_bwd": [_TP] * 6 + [ctypes.c_void_p]}.items():
+                fn = getattr(lib, "mss_" + name)
+                fn.restype, fn.argtypes = ctypes.c_int, args
             lib.mss_release_workspaces.restype = ctypes.c_int
             lib.mss_release_workspaces.argtypes = []
             lib.mss_set_plan_overrides.restype = ctypes.c_int
@@ -315,7 +333,8 @@ def _desc(t):
         raise ValueError("libmamba_scan takes device tensors")
     if _DTYPES is None:
         import torch
-        _DTYPES = {torch.float32: MSS_F32, torch.bfloat16: MSS_BF16, torch.int32: MSS_I32}
+        _DTYPES = {torch.float32: MSS_F32, torch.bfloat16: MSS_BF16, torch.int32: MSS_I32,
+                   torch.float8_e4m3fn: MSS_F8E4M3}
     shape, stride = tuple(t.shape), t.stride()
     n = len(shape)
     if n > 4:

@@ -103,7 +103,7 @@ def _native():
         except ImportError as e:
             raise RuntimeError(f"the _native module is missing ({e}): build it with "
                                "`python -m selective_state_space_06_amd.build`") from e
-        m.set_dtypes(torch.float32, torch.bfloat16, torch.int32)
+        m.set_dtypes(torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn)
         _native_module = m
     return _native_module
 

@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmamba_scan.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["abi.hip", "scan_fwd.hip", "scan_fast.hip", "scan_bwd.hip", "state_update.hip", "conv1d.hip",
-           "ssd_scan.hip", "gated_scan.hip", "conv1d_bwd.hip", "beam.hip", "abi_recurrent.hip"]
+           "ssd_scan.hip", "gated_scan.hip", "conv1d_bwd.hip", "beam.hip", "abi_recurrent.hip",
+           "rms_norm.hip", "linear_attention.hip", "token_logprobs.hip", "abi_layers.hip"]
 ARCH = "gfx950"
 
 
@@ -153,7 +154,7 @@ def build(verbose: bool = False, extra: list[str] | None = None) -> str:
         build_native(verbose)
     else:  # the library is whole without it; its absence is reported where it is used
         sys.stderr.write("Python's headers are missing: _native, which the torch front end of the gated scan, the conv's "
-                         "gradients and beam search needs, is not built\n")
+                         "gradients, beam search, norms, linear attention and log probabilities needs, is not built\n")
     return LIB_PATH
 
 

@@ -17,7 +17,7 @@ inline int64_t numel(const mss_tensor_t& t) {
     return n;
 }
 
-inline size_t elem_size(int32_t dtype) { return dtype == MSS_BF16 ? 2 : 4; }
+inline size_t elem_size(int32_t dtype) { return dtype == MSS_F8E4M3 ? 1 : dtype == MSS_BF16 ? 2 : 4; }
 
 inline bool shape_is(const mss_tensor_t& t, int ndim, int64_t s0, int64_t s1 = 0, int64_t s2 = 0, int64_t s3 = 0) {
     if (t.ndim != ndim) return false;
@@ -83,6 +83,58 @@ int check_descs(const mss_tensor_t* const (&req)[K], std::initializer_list<const
         if (s != MSS_OK) return s;
     }
     return MSS_OK;
+}
+
+using Ts = std::initializer_list<const mss_tensor_t*>;
+
+inline bool act_dtype(int32_t d) { return d == MSS_F32 || d == MSS_BF16; }
+
+inline bool all_dtype(Ts ts, int32_t d) {
+    for (const mss_tensor_t* t : ts)
+        if (t && t->dtype != d) return false;
+    return true;
+}
+
+// Dense, element-aligned.
+inline bool laid_out(Ts ts) {
+    for (const mss_tensor_t* t : ts)
+        if (t && (!dense(*t) || !aligned(*t, elem_size(t->dtype)))) return false;
+    return true;
+}
+
+// No output overlaps an input or another output.
+inline bool apart(Ts ins, Ts outs) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const mss_tensor_t* t : ins)
+            if (overlap(*o, t)) return false;
+        for (auto p = o + 1; p != outs.end(); ++p)
+            if (overlap(*o, *p)) return false;
+    }
+    return true;
+}
+
+// Scratch of at least n floats, 16-byte aligned; may be NULL when n is 0.
+inline int check_scratch(const mss_tensor_t* t, int64_t n) {
+    if (n == 0 && !t) return MSS_OK;
+    if (!t) return MSS_ERR_NULL_ARG;
+    const int s = check_desc(t, true);
+    if (s != MSS_OK) return s;
+    if (t->ndim != 1 || t->shape[0] < n) return MSS_ERR_SHAPE;
+    if (t->dtype != MSS_F32) return MSS_ERR_DTYPE;
+    if (!dense(*t) || !aligned(*t, 16)) return MSS_ERR_LAYOUT;
+    return MSS_OK;
+}
+
+template <class T>
+T* ptr(const mss_tensor_t* t) {
+    return t && numel(*t) > 0 ? static_cast<T*>(t->data) : nullptr;
+}
+
+inline bool whole_vectors(int64_t row, int32_t dtype, Ts ts) {
+    if (row * static_cast<int64_t>(elem_size(dtype)) % 16 != 0) return false;
+    for (const mss_tensor_t* t : ts)
+        if (t && !aligned(*t, 16)) return false;
+    return true;
 }
 
 }  // namespace abi

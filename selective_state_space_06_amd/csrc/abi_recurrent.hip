@@ -12,57 +12,6 @@
 namespace {
 
 using namespace mss::abi;
-using Ts = std::initializer_list<const mss_tensor_t*>;
-
-bool act_dtype(int32_t d) { return d == MSS_F32 || d == MSS_BF16; }
-
-bool all_dtype(Ts ts, int32_t d) {
-    for (const mss_tensor_t* t : ts)
-        if (t && t->dtype != d) return false;
-    return true;
-}
-
-// Dense, element-aligned.
-bool laid_out(Ts ts) {
-    for (const mss_tensor_t* t : ts)
-        if (t && (!dense(*t) || !aligned(*t, elem_size(t->dtype)))) return false;
-    return true;
-}
-
-// No output overlaps an input or another output.
-bool apart(Ts ins, Ts outs) {
-    for (auto o = outs.begin(); o != outs.end(); ++o) {
-        for (const mss_tensor_t* t : ins)
-            if (overlap(*o, t)) return false;
-        for (auto p = o + 1; p != outs.end(); ++p)
-            if (overlap(*o, *p)) return false;
-    }
-    return true;
-}
-
-// Scratch of at least n floats, 16-byte aligned; may be NULL when n is 0.
-int check_scratch(const mss_tensor_t* t, int64_t n) {
-    if (n == 0 && !t) return MSS_OK;
-    if (!t) return MSS_ERR_NULL_ARG;
-    const int s = check_desc(t, true);
-    if (s != MSS_OK) return s;
-    if (t->ndim != 1 || t->shape[0] < n) return MSS_ERR_SHAPE;
-    if (t->dtype != MSS_F32) return MSS_ERR_DTYPE;
-    if (!dense(*t) || !aligned(*t, 16)) return MSS_ERR_LAYOUT;
-    return MSS_OK;
-}
-
-template <class T>
-T* ptr(const mss_tensor_t* t) {
-    return t && numel(*t) > 0 ? static_cast<T*>(t->data) : nullptr;
-}
-
-bool whole_vectors(int64_t row, int32_t dtype, Ts ts) {
-    if (row * static_cast<int64_t>(elem_size(dtype)) % 16 != 0) return false;
-    for (const mss_tensor_t* t : ts)
-        if (t && !aligned(*t, 16)) return false;
-    return true;
-}
 
 int status(hipError_t e) { return e == hipSuccess ? MSS_OK : MSS_ERR_HIP; }
 

@@ -260,4 +260,109 @@ hipError_t launch_beam_select(const BeamSelectLaunch& a, hipStream_t stream);
 hipError_t launch_beam_reorder(const BeamReorderLaunch* states, int count, const int32_t* parents, int64_t Bt, int N,
                                hipStream_t stream);
 
+// RMS norm (rms_norm.hip): rows of W columns.
+constexpr int64_t kNormWidest = 16384;
+
+struct NormLaunch {
+    const void* x;
+    const void* residual;        // nullable
+    const float* weight;
+    void* out;                   // the type of x; e4m3 with scales
+    void* residual_out;          // with residual
+    float* rstd;                 // (R), nullable
+    float* scales;               // (R, G), nullable
+    int64_t R, W;
+    float eps;
+    int G;                       // 1, or ceil(W / 128)
+    bool x_bf16, residual_bf16;
+    bool vec_ok;                 // rows of every tensor are whole aligned 16-byte vectors (8-byte ones in e4m3)
+};
+struct NormBwdLaunch {
+    const void* z;
+    const float* weight;
+    const float* rstd;
+    const void* dout;
+    const void* dresidual_out;   // nullable
+    void* dx;                    // the type of dout
+    void* dresidual;             // the type of z, nullable
+    float* dweight;              // nullable
+    float* scratch;              // with dweight
+    int64_t R, W;
+    bool x_bf16, z_bf16, vec_ok;
+};
+int64_t rms_norm_bwd_scratch(int64_t R, int64_t W);
+hipError_t launch_rms_norm_fwd(const NormLaunch& a, hipStream_t stream);
+hipError_t launch_rms_norm_bwd(const NormBwdLaunch& a, hipStream_t stream);
+
+// Linear attention (linear_attention.hip): rows (Bt, L, heads, dim), states (Bt, H, K, V).
+constexpr int kAttnMostDim = 128;
+
+struct AttnLaunch {
+    const void* q;               // (Bt, L, Hq, K)
+    const void* k;               // (Bt, L, Hk, K)
+    const void* v;               // (Bt, L, Hv, V)
+    const float* rate;           // (H)
+    const float* h0 = nullptr;   // nullable
+    const int32_t* lens = nullptr;  // (Bt), nullable
+    void* out = nullptr;         // (Bt, L, H, V), nullable
+    float* last_state = nullptr; // nullable
+    // the backward's
+    const void* dout = nullptr;  // (Bt, L, H, V)
+    const float* dlast = nullptr;   // nullable
+    void* dq = nullptr;
+    void* dk = nullptr;
+    void* dv = nullptr;
+    float* dh0 = nullptr;        // nullable
+    float* scratch = nullptr;
+    int64_t Bt = 0, L = 0;
+    int H = 0, Hq = 0, Hk = 0, Hv = 0, K = 0, V = 0;
+    float scale = 1.0f;
+    bool bf16 = false;
+};
+struct AttnUpdateLaunch {
+    float* state;                // (Bt, H, K, V), in/out
+    const void* q;               // (Bt, Hq, K)
+    const void* k;               // (Bt, Hk, K)
+    const void* v;               // (Bt, Hv, V)
+    const float* rate;
+    void* out;                   // (Bt, H, V)
+    int64_t Bt;
+    int H, Hq, Hk, Hv, K, V;
+    float scale;
+    bool bf16;
+};
+int64_t attn_fwd_scratch(int64_t Bt, int64_t L, int H, int K, int V);
+int64_t attn_bwd_scratch(int64_t Bt, int64_t L, int H, int Hq, int Hk, int Hv, int K, int V);
+hipError_t launch_attn_fwd(const AttnLaunch& a, hipStream_t stream);
+hipError_t launch_attn_bwd(const AttnLaunch& a, hipStream_t stream);
+hipError_t launch_attn_update(const AttnUpdateLaunch& a, hipStream_t stream);
+
+// Token log probabilities (token_logprobs.hip): rows of V logits.
+struct LogprobLaunch {
+    const void* logits;          // (R, V)
+    const int32_t* tokens;       // (R)
+    float* logprobs;             // (R)
+    float* entropy;              // (R), nullable
+    float* top_logprobs;         // (R, K), nullable
+    int32_t* top_tokens;         // (R, K)
+    float* saved;                // (R, 3), nullable
+    float* scratch;
+    int64_t R, V;
+    int K;                       // 0: no alternatives
+    bool bf16, vec_ok;
+};
+struct LogprobBwdLaunch {
+    const void* logits;
+    const int32_t* tokens;
+    const float* saved;
+    const float* dlogprobs;      // (R)
+    const float* dentropy;       // (R), nullable
+    void* dlogits;               // (R, V); may be logits
+    int64_t R, V;
+    bool bf16, vec_ok;
+};
+int64_t logprob_scratch(int64_t R, int64_t V, int64_t K);
+hipError_t launch_logprob_fwd(const LogprobLaunch& a, hipStream_t stream);
+hipError_t launch_logprob_bwd(const LogprobBwdLaunch& a, hipStream_t stream);
+
 }  // namespace mss

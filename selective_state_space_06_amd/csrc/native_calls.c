@@ -20,7 +20,7 @@
 enum { MOST = 16 };
 
 static PyObject *s_data_ptr, *s_dtype, *s_shape, *s_stride, *s_is_contiguous, *s_get_device;
-static PyObject *dtypes[3]; /* torch.float32, torch.bfloat16, torch.int32, in the order of mss_dtype_t */
+static PyObject *dtypes[4]; /* torch's types in the order of mss_dtype_t */
 
 static int whole(PyObject* o, int64_t* v) {
     *v = PyLong_AsLongLong(o);
@@ -78,7 +78,7 @@ static int describe(PyObject* t, mss_tensor_t* d, int64_t* device) {
     PyObject* dtype = PyObject_GetAttr(t, s_dtype);
     if (!dtype) return -1;
     d->dtype = -1; /* any other type: refused by the library */
-    for (int k = 0; k < 3; ++k)
+    for (int k = 0; k < 4; ++k)
         if (dtype == dtypes[k]) d->dtype = k;
     Py_DECREF(dtype);
     if (four(PyObject_GetAttr(t, s_shape), d->shape, &d->ndim)) return -1;
@@ -97,12 +97,13 @@ static int describe(PyObject* t, mss_tensor_t* d, int64_t* device) {
     return four(PyObject_CallMethodNoArgs(t, s_stride), d->stride, &n);
 }
 
-/* The arguments of a call: descriptors p[k] (NULL for None) and whole numbers v[k], as `kinds` says
- * ('t' a tensor or None, 'i' a whole number), and the stream that ends them. */
+/* The arguments of a call: descriptors p[k] (NULL for None), whole numbers v[k] and others f[k], as `kinds` says
+ * ('t' a tensor or None, 'i' a whole number, 'f' a number), and the stream that ends them. */
 typedef struct {
     mss_tensor_t d[MOST];
     const mss_tensor_t* p[MOST];
     int v[MOST];
+    float f[MOST];
     void* stream;
 } Call;
 
@@ -123,6 +124,10 @@ static int take(Call* c, const char* kinds, PyObject* const* args, Py_ssize_t n)
                 return -1;
             }
             c->v[k] = (int)v;
+        } else if (kinds[k] == 'f') {
+            const double v = PyFloat_AsDouble(args[k]);
+            if (v == -1.0 && PyErr_Occurred()) return -1;
+            c->f[k] = (float)v;
         } else if (args[k] != Py_None) {
             if (describe(args[k], &c->d[k], &device)) return -1;
             c->p[k] = &c->d[k];
@@ -153,6 +158,19 @@ ENTRY(causal_conv1d_bwd, "ttttittttttt",
       mss_causal_conv1d_bwd(P[0], P[1], P[2], P[3], c.v[4], P[5], P[6], P[7], P[8], P[9], P[10], P[11], c.stream))
 ENTRY(beam_select, "tttittttt",
       mss_beam_select(P[0], P[1], P[2], c.v[3], P[4], P[5], P[6], P[7], P[8], c.stream))
+ENTRY(rms_norm_fwd, "tttftttt",
+      mss_rms_norm_fwd(P[0], P[1], P[2], c.f[3], P[4], P[5], P[6], P[7], c.stream))
+ENTRY(rms_norm_bwd, "ttttttttt", mss_rms_norm_bwd(P[0], P[1], P[2], P[3], P[4], P[5], P[6], P[7], P[8], c.stream))
+ENTRY(linear_attention_fwd, "ttttfttttt",
+      mss_linear_attention_fwd(P[0], P[1], P[2], P[3], c.f[4], P[5], P[6], P[7], P[8], P[9], c.stream))
+ENTRY(linear_attention_bwd, "ttttfttttttttt",
+      mss_linear_attention_bwd(P[0], P[1], P[2], P[3], c.f[4], P[5], P[6], P[7], P[8], P[9], P[10], P[11], P[12], P[13],
+                               c.stream))
+ENTRY(linear_attention_update, "tttttft",
+      mss_linear_attention_update(P[0], P[1], P[2], P[3], P[4], c.f[5], P[6], c.stream))
+ENTRY(token_logprobs_fwd, "tttttttt",
+      mss_token_logprobs_fwd(P[0], P[1], P[2], P[3], P[4], P[5], P[6], P[7], c.stream))
+ENTRY(token_logprobs_bwd, "tttttt", mss_token_logprobs_bwd(P[0], P[1], P[2], P[3], P[4], P[5], c.stream))
 #undef P
 
 /* beam_reorder(sequence of tensors, parents, stream) */
@@ -222,14 +240,36 @@ static PyObject* beam_select_scratch(PyObject* self, PyObject* const* args, Py_s
     return Py_BuildValue("iL", st, (long long)floats);
 }
 
-/* set_dtypes(torch.float32, torch.bfloat16, torch.int32) */
+static PyObject* rms_norm_bwd_scratch(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+    (void)self;
+    int64_t v[2], floats = 0;
+    if (sizes(args, n, v, 2)) return NULL;
+    const int st = mss_rms_norm_bwd_scratch(v[0], v[1], &floats);
+    return Py_BuildValue("iL", st, (long long)floats);
+}
+static PyObject* linear_attention_scratch(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+    (void)self;
+    int64_t v[8], fwd = 0, bwd = 0;
+    if (sizes(args, n, v, 8)) return NULL;
+    const int st = mss_linear_attention_scratch(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], &fwd, &bwd);
+    return Py_BuildValue("iLL", st, (long long)fwd, (long long)bwd);
+}
+static PyObject* token_logprobs_scratch(PyObject* self, PyObject* const* args, Py_ssize_t n) {
+    (void)self;
+    int64_t v[3], floats = 0;
+    if (sizes(args, n, v, 3)) return NULL;
+    const int st = mss_token_logprobs_scratch(v[0], v[1], v[2], &floats);
+    return Py_BuildValue("iL", st, (long long)floats);
+}
+
+/* set_dtypes(torch.float32, torch.bfloat16, torch.int32, torch.float8_e4m3fn) */
 static PyObject* set_dtypes(PyObject* self, PyObject* const* args, Py_ssize_t n) {
     (void)self;
-    if (n != 3) {
-        PyErr_SetString(PyExc_TypeError, "three types wanted");
+    if (n != 4) {
+        PyErr_SetString(PyExc_TypeError, "four types wanted");
         return NULL;
     }
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 4; ++k) {
         Py_INCREF(args[k]);
         Py_XSETREF(dtypes[k], args[k]);
     }
@@ -240,7 +280,12 @@ static PyObject* set_dtypes(PyObject* self, PyObject* const* args, Py_ssize_t n)
 static PyMethodDef methods[] = {METHOD(gated_scan_fwd),    METHOD(gated_scan_bwd), METHOD(gated_state_update),
                                 METHOD(causal_conv1d_bwd), METHOD(beam_select),    METHOD(beam_reorder),
                                 METHOD(gated_scan_scratch), METHOD(causal_conv1d_bwd_scratch),
-                                METHOD(beam_select_scratch), METHOD(set_dtypes), {NULL, NULL, 0, NULL}};
+                                METHOD(beam_select_scratch), METHOD(rms_norm_fwd), METHOD(rms_norm_bwd),
+                                METHOD(linear_attention_fwd), METHOD(linear_attention_bwd),
+                                METHOD(linear_attention_update), METHOD(token_logprobs_fwd),
+                                METHOD(token_logprobs_bwd), METHOD(rms_norm_bwd_scratch),
+                                METHOD(linear_attention_scratch), METHOD(token_logprobs_scratch),
+                                METHOD(set_dtypes), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__native(void) {
