@@ -3,6 +3,8 @@
 // caller).
 #include <limits.h>
 
+#include <algorithm>
+
 #include "abi_checks.hpp"
 #include "mamba_scan.h"
 #include "mss_internal.hpp"
@@ -30,6 +32,7 @@ bool in_place(const mss_tensor_t* out, const mss_tensor_t* in) { return out && i
 int check_sizes(int64_t Bt, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V) {
     if (Bt < 0 || L < 0 || H < 1 || Hq < 1 || Hk < 1 || Hv < 1 || K < 1 || V < 1) return MSS_ERR_SHAPE;
     if (H % Hq || H % Hk || H % Hv) return MSS_ERR_SHAPE;
+    if (H > 32768) return MSS_ERR_UNSUPPORTED;  // a chunk's offsets are 32 bits
     if (K % 16 || V % 16 || K > mss::kAttnMostDim || V > mss::kAttnMostDim) return MSS_ERR_UNSUPPORTED;
     int64_t n = 0;
     if (__builtin_mul_overflow(Bt, H, &n) || n > (int64_t{1} << 28)) return MSS_ERR_UNSUPPORTED;  // blocks
@@ -141,7 +144,10 @@ int mss_linear_attention_scratch(int64_t batch, int64_t L, int64_t heads, int64_
     if (st != MSS_OK) return st;
     const auto n = [](int64_t v) { return static_cast<int>(v); };
     *fwd = mss::attn_fwd_scratch(batch, L, n(heads), n(key_dim), n(value_dim));
-    *bwd = mss::attn_bwd_scratch(batch, L, n(heads), n(q_heads), n(k_heads), n(v_heads), n(key_dim), n(value_dim));
+    *bwd = 0;
+    for (const bool bf16 : {false, true})  // what either type needs
+        *bwd = std::max(*bwd, mss::attn_bwd_scratch(batch, L, n(heads), n(q_heads), n(k_heads), n(v_heads), n(key_dim),
+                                                    n(value_dim), bf16));
     return MSS_OK;
 }
 
@@ -225,7 +231,7 @@ int mss_linear_attention_bwd(const mss_tensor_t* q, const mss_tensor_t* k, const
         a.Hv = static_cast<int>(Hv); a.K = static_cast<int>(K); a.V = static_cast<int>(V);
         a.scale = scale;
         a.bf16 = q->dtype == MSS_BF16;
-        st = check_scratch(scratch, mss::attn_bwd_scratch(Bt, L, a.H, a.Hq, a.Hk, a.Hv, a.K, a.V));
+        st = check_scratch(scratch, mss::attn_bwd_scratch(Bt, L, a.H, a.Hq, a.Hk, a.Hv, a.K, a.V, a.bf16));
         if (st != MSS_OK) return st;
         a.scratch = ptr<float>(scratch);
         if (!apart({q, k, v, rate, initial_state, seq_lens, dout, dlast_state}, {dq, dk, dv, dinitial_state, scratch}))

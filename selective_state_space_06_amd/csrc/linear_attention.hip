@@ -9,17 +9,34 @@
 // transposed state; dv and dk backwards in time from (k, q, dout) and (v, dout, q), with dlast_state in front.  So one
 // kernel serves all of them, by the tensors it is given, the order in which it takes the rows, and where the scale goes.
 //
-// A block holds a slice of 64 value columns of one head: its four waves 16 columns each, the state's rows of these
-// columns in registers (fp32) all along the sequence.  Queries, keys and values of a chunk go through LDS; the next
-// chunk's are on their way meanwhile.  Scores and state pass from product to product in registers: a product's result
-// (lane: a column, four consecutive rows) is the next product's operand as it stands, when the other operand's rows are
-// taken in the same order.
+// A block walks a head's sequence, or a segment of it, in chunks of 32 steps.  A wave has 16 value columns and keeps the
+// state's rows of these columns in registers (fp32) all along: 32 registers for 128 keys; a block has all columns of the
+// head, four waves or eight, so that queries and keys are read once.  Queries, keys and values of a chunk go through LDS;
+// the next chunk's are on their way meanwhile, by loads that give 0 outside of the chunk instead of being branched
+// around.  The scores of a chunk are made once for the block, a 16 x 16 tile a wave, and shared through LDS; states and
+// values pass from product to product in registers: a product's result (lane: a column, four consecutive rows) is the
+// next product's operand as it stands, when the other operand's rows are taken in the same order, and what has to be
+// turned is read from LDS by the instruction that turns.
+//
+// What bounds it: neither memory nor the matrix cores, but the instructions of a chunk and their waits, 2.2 us for 32 steps
+// with 128 x 128 state, of which decaying the state, cutting it into parts and reading it turned are most.  So what counts
+// is blocks on a CU at once: chunks of 64 steps have twice the scores' work and fewer fit, chunks of 16 leave half of the
+// matrix instruction empty.  A long sequence with few heads is cut into
+// segments; the states between them come from a pass over keys and values alone, whose parts are added up by the block that
+// reads them (up to eight) or by a kernel of their own.
+// The gradients of shared heads are sums over the heads of a group: a block does as many of them side by side as 16 waves
+// hold and adds the outputs up in LDS, in their order; what is left goes through memory and attention_groups_kernel
+// (4 x 2048 x 80 heads, of queries and keys 8: 553 us for the three gradients, 600 with all through memory).
 //
 // bf16 products of fp32 values: a value is cut into bf16 parts (hi = bf16(x), mid = bf16(x - hi), ...), each exact,
 // and the products of parts that matter are summed in fp32.  bf16 inputs are one part; states and scores, met by a
 // rounding to bf16 of the output, are taken in two (2^-17), the decayed values that enter the state in three (2^-25).
 // fp32 inputs are three parts everywhere, with the six products down to 2^-24 (2.7 times the rate of the fp32 matrix
 // instruction).
+//
+// Measured, with both types' own sizes: 4 x 2048 x 32 heads of 128 x 128 bf16 109 us (2.5 TB/s, 158 TFLOP/s of the formula's
+// products); 1 x 32768 x 16 heads of 64 x 64 f32 197 us, of them states 64 and their sums 19; output and gradients of
+// 4 x 2048 x 80 heads of 128 x 64 bf16 with queries and keys of 8 heads 689 us, of 3 x 1531 x 12 heads of 64 x 96 f32 204.
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -32,6 +49,8 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct Rows {          // (Bt, L, heads, dim)
     const void* p;
@@ -44,17 +63,27 @@ struct AArgs {
     const int32_t* lens;     // (Bt), nullable
     const float* init;       // state before (Bt, H, Kd, Vd), or (Bt, H, Vd, Kd) with init_t; nullable
     float* last;             // state after, laid out alike; nullable
-    float* segs;             // (Bt, H, nseg, Kd, Vd): states entering the segments (of 64 seg_len steps)
-    void* out;               // (Bt, L, H, Vd)
+    float* parts;            // (Bt, H, nparts, Kd, Vd): what the parts of all segments but the last add to the state
+    void* out;               // (Bt, L, outs, Vd)
     int64_t Bt, L;
-    int H, Kd, Vd, nseg;
-    int64_t seg_steps;       // a multiple of 64
+    int H, Kd, Vd;
+    int each, outs;          // heads of a group, whose outputs are summed (1: none are); outputs: H, or groups times the
+                             // blocks of a group
+    int nseg, nparts;        // segments; parts of them: `cuts` to each but the last
+    int cuts;
+    int64_t part_steps;      // a multiple of 64
     float s_add, s_out;      // factors of what enters the state, and of the outputs
     bool turned;             // init and last are (Vd, Kd)
     bool back;               // rows in reverse order
 };
+constexpr int kMostWalks = 3;
+struct Walks {  // of one launch: those of the same sizes side by side, so that there are blocks for every CU
+    AArgs w[kMostWalks];
+    int64_t each;  // blocks of a walk
+};
 
-constexpr int kWaves = 4, kVTile = 16 * kWaves;
+constexpr int kFold = 8;  // more parts than these are joined by a kernel of their own
+constexpr int kChunk = 32;  // steps
 constexpr float kMostRate = 1e30f;  // beyond it l^n is 0 for every n but 0, which 0 times infinity would not be
 
 __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
@@ -68,36 +97,47 @@ __device__ __forceinline__ s16x4 turn4(const uint16_t* p) {
 }
 __device__ __forceinline__ s16x8 join8(s16x4 a, s16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
-// Eight floats as N bf16 parts.
-template <int N>
-__device__ __forceinline__ void cut(const float* x, s16x8* part) {
-    float r[8];
+// x minus the low or the high half of a word of two bf16: exact, and one instruction.  The factors (-1, 0) and (0, -1) are
+// kept in registers: as an inline constant of the instruction, -1.0 is not the pair that the compiler takes it for.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ float less_half(float x, uint32_t w, uint32_t factors) {
+    asm("" : "+s"(factors));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, factors), x, false);
+}
+__device__ __forceinline__ float less_lo(float x, uint32_t w) { return less_half(x, w, 0x0000BF80u); }
+__device__ __forceinline__ float less_hi(float x, uint32_t w) { return less_half(x, w, 0xBF800000u); }
+// M pairs of floats as N words of bf16 parts each; r is left with what the parts lack.
+template <int N, int M>
+__device__ __forceinline__ void cut_words(float* r, uint32_t (*w)[M]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = x[e];
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w[e] = pack_bf16x2(r[2 * e], r[2 * e + 1]);
+        for (int e = 0; e < M; ++e) {
+            w[n][e] = pack_bf16x2(r[2 * e], r[2 * e + 1]);
             if (n + 1 < N) {
-                r[2 * e] -= bf16_lo(w[e]);
-                r[2 * e + 1] -= bf16_hi(w[e]);
+                r[2 * e] = less_lo(r[2 * e], w[n][e]);
+                r[2 * e + 1] = less_hi(r[2 * e + 1], w[n][e]);
             }
         }
-        part[n] = __builtin_bit_cast(s16x8, make_uint4(w[0], w[1], w[2], w[3]));
-    }
+}
+// Eight floats as N bf16 parts.
+template <int N>
+__device__ __forceinline__ void cut(float* x, s16x8* part) {
+    uint32_t w[N][4];
+    cut_words<N, 4>(x, w);
+#pragma unroll
+    for (int n = 0; n < N; ++n) part[n] = __builtin_bit_cast(s16x8, make_uint4(w[n][0], w[n][1], w[n][2], w[n][3]));
 }
 
 template <class E>
 struct Form;
 template <>
 struct Form<BF16> {
-    static constexpr int C = 64, NP = 1, NS = 2;  // steps a chunk; parts of inputs; of states and scores
+    static constexpr int NP = 1, NS = 2;  // parts of inputs; of states and scores
 };
 template <>
 struct Form<F32> {
-    static constexpr int C = 32, NP = 3, NS = 3;
+    static constexpr int NP = 3, NS = 3;
 };
 
 // sum of products of parts a (NA) and b (NB), down to the least part of either that is kept
@@ -112,68 +152,130 @@ __device__ __forceinline__ f32x4 mma_parts(const s16x8* a, const s16x8* b, f32x4
     return c;
 }
 
-// STATES: only the state that a segment adds, from zero.  OUT: the outputs' type.
-template <class E, class OUT, int KD, bool STATES>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AArgs a) {
+// N tiles of such sums, part by part: products that follow each other do not wait for each other.
+template <int N, int NA, int NB, class A, class B>
+__device__ __forceinline__ void mma_each(A a, B b, f32x4* c) {
+    constexpr int most = NA > NB ? NA : NB;
+#pragma unroll
+    for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+        for (int j = NB - 1; j >= 0; --j)
+            if (i + j < most) {
+#pragma unroll
+                for (int n = 0; n < N; ++n) c[n] = mma(a(n)[i], b(n)[j], c[n]);
+            }
+}
+
+// The LDS reads before this are issued before what comes after it (the compiler would issue each in front of its use).
+__device__ __forceinline__ void issue_reads() { __builtin_amdgcn_sched_barrier(0); }
+
+// l^n - 1 for the steps n that a state decays by in part i of a sequence of len steps.
+__device__ __forceinline__ float part_decay(const AArgs& a, float rate, int64_t len, int i) {
+    int64_t n = len - i * a.part_steps;
+    n = n < 0 ? 0 : n < a.part_steps ? n : a.part_steps;
+    if (n > 0 && i == 0 && a.back) --n;
+    return expm1f(-rate * static_cast<float>(n));
+}
+
+// Waves a SIMD that a kernel's registers leave room for: as many as its LDS does.
+constexpr int waves_wanted(bool bf16, int KD, int NW, bool states) {
+    return bf16 ? 4 : KD == 128 && NW == 4 ? (states ? 2 : 1) : states && KD == 64 ? 4 : 2;
+}
+
+// STATES: only the state that a part of a segment adds, from zero.  OUT: the outputs' type.  NW: waves, 16 columns each.
+// SUB: heads of a group that a block does side by side, NW waves each, and whose outputs it sums.
+template <class E, class OUT, int KD, int NW, int SUB, bool STATES>
+__global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, NW, STATES)) void attention_kernel(Walks all) {
+    const AArgs& a = all.w[blockIdx.x / all.each];
+    const int64_t block = blockIdx.x % all.each;
     using F = Form<E>;
-    using S = typename E::storage;
-    constexpr int C = F::C, NP = F::NP, NS = F::NS, MT = C / 16, M2 = C / 32, KJ = KD / 32;
-    constexpr int QS = KD + 8, VS = kVTile + 8;              // elements between two rows in LDS
-    constexpr int NQ = C * KD / 8 / 256, NV = C * kVTile / 8 / 256;
-    __shared__ __align__(16) uint16_t qs[STATES ? 1 : NP][STATES ? 1 : C][STATES ? 8 : QS];
-    __shared__ __align__(16) uint16_t ks[NP][C][QS];
-    __shared__ __align__(16) uint16_t vs[NP][C][VS];
+    using O = typename OUT::storage;
+    constexpr int C = kChunk, NP = F::NP, NS = F::NS, MT = C / 16, M2 = C / 32, KJ = KD / 32, KT = KD / 16;
+    constexpr int T = 64 * NW, VT = 16 * NW;                 // threads and columns of a block
+    // Elements between two rows in LDS, which has 64 banks of four bytes.  Rows that lanes read 16 bytes of (queries, scores)
+    // lie an odd multiple of eight banks apart (1 KB in 4.4 cycles; 8.4 at four banks).  Rows read turned, and rows of both
+    // uses, also have their columns moved by bits of the row (key_at, value_at), so that the eight rows of 16 columns that 32
+    // lanes read turned, and the 16 rows of 4 that they read for scores, meet in no bank.
+    constexpr int QS = KD + 16, KS = KD + 32, VS = VT + 16, PS = C + 16;
+    constexpr int QU = KD / 8, VU = VT / 8;                  // units of eight elements a row
+    constexpr int QR = T / QU, VR = T / VU;                  // rows that the block loads at once
+    constexpr int NQ = C > QR ? C / QR : 1, NV = C / VR;     // (f32 with 64 keys: half of eight waves load them)
+    constexpr int ES = sizeof(typename E::storage);
+    __shared__ __align__(16) uint16_t all_qs[SUB][STATES ? 1 : NP][STATES ? 1 : C][STATES ? 8 : QS];
+    __shared__ __align__(16) uint16_t all_ks[SUB][NP][C][KS];
+    __shared__ __align__(16) uint16_t all_vs[SUB][NP][C][VS];
+    __shared__ __align__(16) uint16_t all_ps[SUB][STATES ? 1 : NS][STATES ? 1 : C][STATES ? 8 : PS];  // scores, a step's in a row
+    __shared__ f32x4 others[SUB > 1 ? SUB - 1 : 1][MT][SUB > 1 ? T : 1];  // outputs of the heads but the first
 
-    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    const int vtiles = (a.Vd + kVTile - 1) / kVTile, nseg = STATES ? a.nseg - 1 : a.nseg;
-    const int64_t bh = blockIdx.x / (vtiles * nseg);
-    const int rest = static_cast<int>(blockIdx.x % (vtiles * nseg));
-    const int seg = rest / vtiles, vt = rest % vtiles;
-    const int64_t b = bh / a.H;
-    const int h = static_cast<int>(bh % a.H);
+    const int tid = SUB > 1 ? threadIdx.x % T : threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int sub = SUB > 1 ? __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x / T)) : 0;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    auto& qs = all_qs[sub];
+    auto& ks = all_ks[sub];
+    auto& vs = all_vs[sub];
+    auto& ps = all_ps[sub];
+    const int outs = STATES ? a.H : a.outs, nseg = STATES ? a.nparts : a.nseg;
+    const int64_t b = block / nseg / outs;
+    const int o_head = static_cast<int>(block / nseg % outs), seg = static_cast<int>(block % nseg);
+    // (a group's last block may have fewer heads: the others of its waves go along with nothing)
+    const int in_group = SUB > 1 ? o_head % ((a.each + SUB - 1) / SUB) * SUB + sub : 0;
+    const bool there = SUB == 1 || in_group < a.each;
+    const int h = SUB == 1 ? o_head : o_head / ((a.each + SUB - 1) / SUB) * a.each + (there ? in_group : 0);
+    const int64_t bh = b * a.H + h;
     const int64_t len = a.lens ? (a.lens[b] < 0 ? 0 : a.lens[b] < a.L ? a.lens[b] : a.L) : a.L;
-    const int64_t from = seg * a.seg_steps, to = from + a.seg_steps < a.L ? from + a.seg_steps : a.L;
-    const int v0 = vt * kVTile + wave * 16;                  // this wave's columns
-    const bool mine = v0 < a.Vd;
-    const bool first_whole = a.back;                         // the state enters the first row undecayed
+    const int64_t steps = STATES ? a.part_steps : a.part_steps * a.cuts, from = seg * steps,
+                  to = from + steps < a.L ? from + steps : a.L;
+    const int64_t stop = to < len ? to : len;                // rows past it are 0
+    const int v0 = wave * 16;                                // this wave's columns
+    const bool mine = v0 < a.Vd && there;                    // others go along with zeros
 
-    const auto row_of = [&](const Rows& t, int dim) MSS_INLINED {
-        return static_cast<const S*>(t.p) + (b * a.L * t.heads + h / (a.H / t.heads)) * dim;
+    // Rows of a chunk in the order of the walk: row r is token at + r, or, walked backwards, len - 1 - at - r.  A chunk of n
+    // rows of a tensor is a buffer that begins at its lowest token; a thread's place in it is an offset.  Rows behind the
+    // end and columns beside the head's lie outside of it, where loads give 0 and stores do nothing.
+    const bool back = a.back;
+    const auto buffer_of = [&](const void* t, int heads, int head, int dim, int64_t at, int n, int size) MSS_INLINED {
+        const int64_t token = back ? len - at - n : at;
+        const char* p = static_cast<const char*>(t) + ((b * a.L + token) * heads + head) * dim * static_cast<int64_t>(size);
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, n * heads * dim * size, 0x00027000);
     };
-    const S* qp = row_of(a.q, a.Kd);
-    const S* kp = row_of(a.k, a.Kd);
-    const S* vp = row_of(a.v, a.Vd);
-    const int64_t qn = static_cast<int64_t>(a.q.heads) * a.Kd, kn = static_cast<int64_t>(a.k.heads) * a.Kd,
-                  vn = static_cast<int64_t>(a.v.heads) * a.Vd;
+    constexpr uint32_t kOutside = 0x80000000u;  // no chunk is as large
+    const auto offset_of = [&](int row, int row_bytes, int col, bool in, int size) MSS_INLINED {
+        return in ? static_cast<uint32_t>((back ? C - 1 - row : row) * row_bytes + col * size) : kOutside;
+    };
+    const int q_row = tid / QU, q_col = tid % QU * 8, v_row = tid / VU, v_col = tid % VU * 8;
+    const int q_bytes = a.q.heads * a.Kd * ES, k_bytes = a.k.heads * a.Kd * ES, v_bytes = a.v.heads * a.Vd * ES,
+              o_bytes = a.outs * a.Vd * static_cast<int>(sizeof(O));
+    const bool q_in = q_col < a.Kd && q_row < C, v_in = v_col < a.Vd;
+    const uint32_t q_off = offset_of(q_row, q_bytes, q_col, q_in, ES), k_off = offset_of(q_row, k_bytes, q_col, q_in, ES),
+                   v_off = offset_of(v_row, v_bytes, v_col, v_in, ES),
+                   o_off = offset_of(r16, o_bytes, v0 + 4 * g, mine, sizeof(O));
 
     Raw<E> rq[STATES ? 1 : NQ], rk[NQ], rv[NV];
-    const auto load_rows = [&](const S* p, int64_t step, int dim, int col0, int64_t at, int units, int u, Raw<E>& r)
-                               MSS_INLINED {
-        const int row = u / units, col = col0 + u % units * 8;
-        const int64_t t = at + row;
+    const auto load = [&](int64_t at, int n) MSS_INLINED {
+        const auto rows = [&](const Rows& t, int dim, int row_bytes, uint32_t off, int step, auto& r) MSS_INLINED {
+            const auto p = buffer_of(t.p, t.heads, h / (a.H / t.heads), dim, at, there ? n : 0, ES);
+            off -= back ? (C - n) * row_bytes : 0;
+            const int next = (back ? -step : step) * row_bytes;
 #pragma unroll
-        for (int j = 0; j < kE / E::kPerVec; ++j) r.q[j] = make_uint4(0, 0, 0, 0);
-        if (t < len && col < dim) {
-            const S* s = p + (a.back ? len - 1 - t : t) * step + col;
+            for (int j = 0; j < static_cast<int>(sizeof(r) / sizeof(r[0])); ++j)
 #pragma unroll
-            for (int j = 0; j < kE / E::kPerVec; ++j) r.q[j] = *reinterpret_cast<const uint4*>(s + j * E::kPerVec);
-        }
+                for (int i = 0; i < kE / E::kPerVec; ++i)
+                    r[j].q[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(p, off + j * next + 16 * i, 0, 0));
+        };
+        if constexpr (!STATES) rows(a.q, a.Kd, q_bytes, q_off, QR, rq);
+        rows(a.k, a.Kd, k_bytes, k_off, QR, rk);
+        rows(a.v, a.Vd, v_bytes, v_off, VR, rv);
     };
-    const auto load = [&](int64_t at) MSS_INLINED {
-#pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-            if constexpr (!STATES) load_rows(qp, qn, a.Kd, 0, at, KD / 8, threadIdx.x + j * 256, rq[j]);
-            load_rows(kp, kn, a.Kd, 0, at, KD / 8, threadIdx.x + j * 256, rk[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            load_rows(vp, vn, a.Vd, vt * kVTile, at, kVTile / 8, threadIdx.x + j * 256, rv[j]);
-    };
-    const auto put = [&](const Raw<E>& r, uint16_t* p, int64_t plane) MSS_INLINED {
+    const auto put = [&](Raw<E> r, uint16_t* p, int plane, bool swap) MSS_INLINED {
         if constexpr (NP == 1) {
-            *reinterpret_cast<uint4*>(p) = r.q[0];
+            const uint4 q = r.q[0];
+            *reinterpret_cast<uint4*>(p) = swap ? make_uint4(q.z, q.w, q.x, q.y) : q;
         } else {
+            if (swap) {
+                const uint4 q = r.q[0];
+                r.q[0] = r.q[1];
+                r.q[1] = q;
+            }
             float x[kE];
             r.unpack(x);
             s16x8 part[NP];
@@ -182,221 +284,290 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AArgs a) {
             for (int n = 0; n < NP; ++n) *reinterpret_cast<s16x8*>(p + n * plane) = part[n];
         }
     };
+    const auto key_at = [](int row, int col) MSS_INLINED { return col ^ (row & 8) >> 1 ^ (row & 4) << 2; };
+    const auto value_at = [](int row, int col) MSS_INLINED { return col ^ (row & 8) * (VT / 32); };
     const auto store = [&]() MSS_INLINED {
+        if (QR <= C || q_row < C) {
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) {
-            const int u = threadIdx.x + j * 256, row = u / (KD / 8), col = u % (KD / 8) * 8;
-            if constexpr (!STATES) put(rq[j], &qs[0][row][col], C * QS);
-            put(rk[j], &ks[0][row][col], C * QS);
+            for (int j = 0; j < NQ; ++j) {
+                const int row = q_row + j * QR;
+                if constexpr (!STATES) put(rq[j], &qs[0][row][q_col], C * QS, false);
+                put(rk[j], &ks[0][row][key_at(row, q_col) & ~7], C * KS, row & 8);  // (halves of 16 bytes as key_at has them)
+            }
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int u = threadIdx.x + j * 256;
-            put(rv[j], &vs[0][u / (kVTile / 8)][u % (kVTile / 8) * 8], C * VS);
+        for (int j = 0; j < NV; ++j) put(rv[j], &vs[0][v_row + j * VR][value_at(v_row + j * VR, v_col)], C * VS, false);
+    };
+    // eight values of a column, rows 32 m + 8 g ...
+    const auto read_values = [&](int m, s16x8* f) MSS_INLINED {
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const uint16_t* s = &vs[p][32 * m + 8 * g + (r16 >> 2)][value_at(8 * g, v0 + 4 * (r16 & 3))];
+            f[p] = join8(turn4(s), turn4(s + 4 * VS));
         }
     };
 
-    // powers of the decay.  A score's lane is a column t = 16 b + r16, its rows s = 16 a + 4 g + i.
+    // Powers of the decay.  A score's lane is a step t = 16 tb + r16, its rows are s = 16 ta + 4 g + i.
     const float rate = fminf(fmaxf(a.rate[h], 0.0f), kMostRate), rl = rate * kLog2e;
     const auto power = [&](int n) MSS_INLINED { return fast_exp2(-rl * static_cast<float>(n)); };
-    float near[4], off[4], tail[4], step16[MT];
+    const auto uniform = [](float x) MSS_INLINED {
+        return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+    };
+    float small[8];  // l^0 .. l^7, in scalar registers: the powers of a lane's rows are products of one of its own and these
+#pragma unroll
+    for (int e = 0; e < 8; ++e) small[e] = uniform(power(e));
+    float near[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) near[i] = power(r16 >= 4 * g + i ? r16 - 4 * g - i : 0) * (a.s_add * a.s_out);
+    const float off = power(13 + r16 - 4 * g) * (a.s_add * a.s_out), since = power(r16) * a.s_out,
+                tail = power(24 - 8 * g) * a.s_add;
+    const float tail32 = uniform(power(32)), less = uniform(expm1f(-rate * C));
+    // steps that the state decays by in a chunk of n rows; walked backwards, it enters the first row undecayed
+    const auto decays = [&](int64_t at, int n) MSS_INLINED { return back && at == 0 ? n - 1 : n; };
+
+    // The state: tile j holds rows 32 (j / 2) + 8 g + 4 (j % 2) + i of a column, so that two tiles are eight rows in turn.
+    f32x4 st[KT];
+    const int64_t per = static_cast<int64_t>(a.Kd) * a.Vd;
+    // every element of the state that there is, with its place in memory (turned: (Vd, Kd))
+    const auto each_of_state = [&](bool turned, auto f) MSS_INLINED {
+        const int nk = turned ? 1 : a.Vd, nv = turned ? a.Kd : 1;
+        const int lane_at = 8 * g * nk + (v0 + r16) * nv;
+        if (!mine) return;
+#pragma unroll
+        for (int j = 0; j < KJ; ++j) {
+            if (32 * j + 8 * g >= a.Kd) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                st[2 * j + i / 4][i % 4] = f(st[2 * j + i / 4][i % 4], lane_at + (32 * j + i) * nk);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < KT; ++j) st[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // where a lane reads keys turned: four rows from 8 g, and the four behind them, in a tile of either kind
+    const uint16_t* turned[2][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int n = r16 - 4 * g - i;
-        near[i] = n >= 0 ? power(n) * (a.s_add * a.s_out) : 0.0f;
-        off[i] = power(16 + n) * (a.s_add * a.s_out);
-        tail[i] = power(15 - 4 * g - i) * a.s_add;
+        const int row = 8 * g + (r16 >> 2) + 4 * (i % 2);
+        turned[i / 2][i % 2] = &ks[0][row][key_at(row, 8 * (r16 & 3) + 4 * (i / 2))];
     }
-#pragma unroll
-    for (int n = 0; n < MT; ++n) step16[n] = power(16 * n);
-    const float since = power(r16 + 1) * a.s_out, since0 = power(r16) * a.s_out;
-    const float less = expm1f(-rate * C);
-
-    // the state: tile j holds rows 32 (j / 2) + 8 g + 4 (j % 2) + i of column v0 + r16
-    f32x4 st[KD / 16];
-    const auto state_at = [&](int j, int i) MSS_INLINED { return 32 * (j / 2) + 8 * g + 4 * (j % 2) + i; };
-#pragma unroll
-    for (int j = 0; j < KD / 16; ++j) {
-        st[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (STATES || !mine) continue;
-        const int v = v0 + r16;
-        const float* from_segs = a.nseg > 1 ? a.segs + (bh * a.nseg + seg) * a.Kd * a.Vd : nullptr;
-        const float* from_init = a.init ? a.init + bh * a.Kd * a.Vd : nullptr;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int k = state_at(j, i);
-            if (k >= a.Kd) continue;
-            if (from_segs) st[j][i] = from_segs[k * a.Vd + v];
-            else if (from_init) st[j][i] = from_init[a.turned ? v * a.Kd + k : k * a.Vd + v];
+    const auto rows_at = [&](int64_t at) MSS_INLINED {  // rows of a chunk
+        const int64_t n = stop - at;
+        return static_cast<int>(n < 0 ? 0 : n < C ? n : C);
+    };
+    load(from, rows_at(from));
+    if constexpr (!STATES) {
+        // the state before the segment: what the join kernel made of it, or the first one and what the parts before add
+        const bool joined = a.nparts > kFold && seg > 0;
+        for (int i = joined ? seg * a.cuts - 1 : -1; i < seg * a.cuts; ++i) {
+            const float* p = i < 0 ? a.init + bh * per : a.parts + (bh * a.nparts + i) * per;
+            const float gone = i < 0 || joined ? 0.0f : part_decay(a, rate, len, i);
+            if (i >= 0 || a.init)
+                each_of_state(i < 0 && a.turned, [&](float x, int j) MSS_INLINED { return fmaf(x, gone, x) + p[j]; });
         }
+        // scores behind a step stay 0: only the others are written
+        for (int e = tid; e < NS * C * PS / 8; e += T) reinterpret_cast<uint4*>(&ps[0][0][0])[e] = make_uint4(0, 0, 0, 0);
     }
 
-    const int64_t stop = to < len ? to : len;  // rows past it are 0
-    if (from < stop) load(from);
+    const auto write = [&](int64_t at, int n, const f32x4* acc) MSS_INLINED {
+                    const auto o = buffer_of(a.out, a.outs, o_head, a.Vd, at, n, sizeof(O));
+                    const uint32_t first = o_off - (back ? (C - n) * o_bytes : 0);
+#pragma unroll
+                    for (int tb = 0; tb < MT; ++tb) {
+                        const uint32_t off = first + (back ? -16 : 16) * tb * o_bytes;
+                        const f32x4 x = acc[tb];
+                        if constexpr (sizeof(O) == 2)
+                            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, o, off, 0, 0);
+                        else
+                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), o, off, 0, 0);
+                    }
+    };
     for (int64_t at = from; at < stop; at += C) {
+        const int n = rows_at(at);
         store();
         __syncthreads();
-        if (at + C < stop) load(at + C);
-        const int n = len - at < C ? static_cast<int>(len - at) : C;  // rows of this chunk
+        load(at + C, rows_at(at + C));
         s16x8 vf[M2][NP];
-        if (mine) {
+        f32x4 acc[MT];
+        if constexpr (!STATES) {
+            // scores: the tiles (ta <= tb) in turn to the waves
+            constexpr int tiles = MT * (MT + 1) / 2;
+            for (int tile = wave; tile < tiles; tile += NW) {
+                int tb = 0, ta = tile;
+                while (ta > tb) ta -= ++tb;
+                s16x8 qf[KJ][NP], kf[KJ][NP];
 #pragma unroll
-            for (int m = 0; m < M2; ++m)
+                for (int j = 0; j < KJ; ++j)
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                    const uint16_t* s = &vs[p][32 * m + 4 * g + (r16 >> 2)][wave * 16 + 4 * (r16 & 3)];
-                    vf[m][p] = join8(turn4(s), turn4(s + 16 * VS));
+                    for (int p = 0; p < NP; ++p) {
+                        qf[j][p] = *reinterpret_cast<const s16x8*>(&qs[p][16 * tb + r16][32 * j + 8 * g]);
+                        const uint16_t* row = ks[p][16 * ta + r16] + 32 * j;  // (key_at moves columns within 32)
+                        kf[j][p] = join8(*reinterpret_cast<const s16x4*>(row + key_at(r16, 8 * g)),
+                                         *reinterpret_cast<const s16x4*>(row + key_at(r16, 8 * g + 4)));
+                    }
+                issue_reads();
+                f32x4 p4 = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int j = 0; j < KJ; ++j) p4 = mma_parts<NP, NP>(kf[j], qf[j], p4);
+                if (ta == tb) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        p4[i] = r16 >= 4 * g + i ? p4[i] * near[i] : 0.0f;
+                    }
+                } else {
+                    const float f = off * power(16 * (tb - ta - 1));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p4[i] *= f * small[3 - i];
                 }
-            if constexpr (!STATES) {
-                s16x8 sf[KJ][NS];
+                uint32_t w[NS][2];
+                float x[4] = {p4[0], p4[1], p4[2], p4[3]};
+                cut_words<NS, 2>(x, w);
 #pragma unroll
-                for (int j = 0; j < KJ; ++j) {
-                    float x[8];
+                for (int p = 0; p < NS; ++p)
+                    *reinterpret_cast<uint2*>(&ps[p][16 * tb + r16][16 * ta + 4 * g]) = make_uint2(w[p][0], w[p][1]);
+            }
+            // what the state before the chunk gives: rows of a tile are columns v, lanes are steps t
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[i] = st[2 * j][i], x[4 + i] = st[2 * j + 1][i];
-                    cut<NS>(x, sf[j]);
-                }
-                const float in = at == 0 && first_whole ? since0 : since;
+            for (int tb = 0; tb < MT; ++tb) acc[tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int tb = 0; tb < MT; ++tb) {
-                    s16x8 qf[KJ][NP];
+            for (int j = 0; j < KJ; ++j) {
+                s16x8 qf[MT][NP], sf[NS];
 #pragma unroll
-                    for (int j = 0; j < KJ; ++j)
+                for (int tb = 0; tb < MT; ++tb)
 #pragma unroll
-                        for (int p = 0; p < NP; ++p)
-                            qf[j][p] = *reinterpret_cast<const s16x8*>(&qs[p][16 * tb + r16][32 * j + 8 * g]);
-                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};  // rows: columns v, lanes: steps t
+                    for (int p = 0; p < NP; ++p)
+                        qf[tb][p] = *reinterpret_cast<const s16x8*>(&qs[p][16 * tb + r16][32 * j + 8 * g]);
+                issue_reads();
+                float x[8];
 #pragma unroll
-                    for (int j = 0; j < KJ; ++j) acc = mma_parts<NS, NP>(sf[j], qf[j], acc);
-                    acc *= in * step16[tb];
-                    float sc[MT][4];
+                for (int i = 0; i < 4; ++i) x[i] = st[2 * j][i], x[4 + i] = st[2 * j + 1][i];
+                cut<NS>(x, sf);
+                mma_each<MT, NS, NP>([&](int) MSS_INLINED { return sf; }, [&](int tb) MSS_INLINED { return qf[tb]; }, acc);
+            }
 #pragma unroll
-                    for (int ta = 0; ta < (tb / 2 + 1) * 2; ++ta) {
-                        if (ta > tb) {
+            for (int tb = 0; tb < MT; ++tb) acc[tb] *= since * power(16 * tb + (back && at == 0 ? 0 : 1));
+            __syncthreads();
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) sc[ta][i] = 0.0f;
-                            continue;
-                        }
-                        f32x4 p4 = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int m = 0; m < M2; ++m) {
+                read_values(m, vf[m]);
 #pragma unroll
-                        for (int j = 0; j < KJ; ++j) {
-                            s16x8 kf[NP];
+                for (int j = NS - 1; j >= 0; --j) {
+                    s16x8 pf[MT];
 #pragma unroll
-                            for (int p = 0; p < NP; ++p)
-                                kf[p] = *reinterpret_cast<const s16x8*>(&ks[p][16 * ta + r16][32 * j + 8 * g]);
-                            p4 = mma_parts<NP, NP>(kf, qf[j], p4);
-                        }
+                    for (int tb = 2 * m; tb < MT; ++tb)
+                        pf[tb] = *reinterpret_cast<const s16x8*>(&ps[j][16 * tb + r16][32 * m + 8 * g]);
+                    issue_reads();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sc[ta][i] = ta < tb ? p4[i] * (off[i] * step16[tb - ta - 1])
-                                                : r16 >= 4 * g + i ? p4[i] * near[i] : 0.0f;
-                    }
+                    for (int i = NP - 1; i >= 0; --i)
 #pragma unroll
-                    for (int m = 0; m <= tb / 2; ++m) {
-                        float x[8];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = sc[2 * m][i], x[4 + i] = sc[2 * m + 1][i];
-                        s16x8 pf[NS];
-                        cut<NS>(x, pf);
-                        acc = mma_parts<NP, NS>(vf[m], pf, acc);
-                    }
-                    const int64_t t = at + 16 * tb + r16;
-                    if (t < stop) {
-                        const int64_t token = a.back ? len - 1 - t : t;
-                        auto* o = static_cast<typename OUT::storage*>(a.out) + ((b * a.L + token) * a.H + h) * a.Vd + v0 + 4 * g;
-                        if (sizeof(typename OUT::storage) == 2) {
-                            *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
-                        } else {
-                            *reinterpret_cast<f32x4*>(o) = acc;
-                        }
-                    }
+                        for (int tb = 2 * m; tb < MT; ++tb)
+                            if (i + j < NS) acc[tb] = mma(vf[m][i], pf[tb], acc[tb]);
                 }
             }
+            if (SUB == 1) write(at, n, acc);
+            else if (sub > 0) {
+#pragma unroll
+                for (int tb = 0; tb < MT; ++tb) others[sub - 1][tb][tid] = acc[tb];
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < M2; ++m) read_values(m, vf[m]);
         }
         // the state after the chunk, if it is read
-        if (mine && (STATES || at + C < stop || (a.last && seg == a.nseg - 1))) {
-            const bool odd = n < C || (at == 0 && first_whole);
-            const float gone = odd ? expm1f(-rate * static_cast<float>(at == 0 && first_whole ? n - 1 : n)) : less;
+        if (STATES || at + C < stop || (a.last && seg == a.nseg - 1)) {
+            const int d = decays(at, n);
+            const float gone = d == C ? less : expm1f(-rate * static_cast<float>(d));
 #pragma unroll
-            for (int j = 0; j < KD / 16; ++j)
+            for (int j = 0; j < KT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) st[j][i] = fmaf(st[j][i], gone, st[j][i]);
 #pragma unroll
             for (int m = 0; m < M2; ++m) {
-                float x[8];
+                float w[8], x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = (m + 1 < M2 ? tail * tail32 : tail) * small[7 - e];
+                if (n < C) {  // rows past the end are zeros
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int s = n - 1 - (32 * m + 8 * g + e);
+                        w[e] = power(s > 0 ? s : 0) * a.s_add;
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    float v = 0.0f;
+                    x[e] = bf16_to_f32(static_cast<uint16_t>(vf[m][0][e]));
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) v += bf16_to_f32(static_cast<uint16_t>(vf[m][p][e]));
-                    const int tile = 2 * m + e / 4, s = 16 * tile + 4 * g + e % 4;
-                    float w = tail[e % 4] * step16[MT - 1 - tile];
-                    if (n < C) w = power(n - 1 - s > 0 ? n - 1 - s : 0) * a.s_add;  // rows past the end are zeros
-                    x[e] = v * w;
+                    for (int p = 1; p < NP; ++p) x[e] += bf16_to_f32(static_cast<uint16_t>(vf[m][p][e]));
+                    x[e] *= w[e];
                 }
                 s16x8 wf[3];
                 cut<3>(x, wf);
+                constexpr int G = 4;  // tiles at once
 #pragma unroll
-                for (int j = 0; j < KD / 16; ++j) {
-                    s16x8 kt[NP];
+                for (int j0 = 0; j0 < KT; j0 += G) {
+                    s16x8 kt[G][NP];
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        const uint16_t* s = &ks[p][32 * m + 4 * g + (r16 >> 2)][32 * (j / 2) + 4 * (j % 2) + 8 * (r16 & 3)];
-                        kt[p] = join8(turn4(s), turn4(s + 16 * QS));
-                    }
-                    st[j] = mma_parts<NP, 3>(kt, wf, st[j]);
+                    for (int j = 0; j < G; ++j)
+#pragma unroll
+                        for (int p = 0; p < NP; ++p) {
+                            const int to = (p * C + 32 * m) * KS + 16 * ((j0 + j) & ~1);
+                            kt[j][p] = join8(turn4(turned[j % 2][0] + to), turn4(turned[j % 2][1] + to));
+                        }
+                    issue_reads();
+                    mma_each<G, NP, 3>([&](int j) MSS_INLINED { return kt[j]; }, [&](int) MSS_INLINED { return wf; }, st + j0);
                 }
             }
         }
         __syncthreads();
+        if (!STATES && SUB > 1 && sub == 0) {  // (the others write theirs again behind two barriers)
+#pragma unroll
+            for (int x = 0; x < SUB - 1; ++x)
+#pragma unroll
+                for (int tb = 0; tb < MT; ++tb) acc[tb] += others[x][tb][tid];
+            write(at, n, acc);
+        }
     }
     if (!mine) return;
-    const int v = v0 + r16;
     if constexpr (STATES) {
-        float* o = a.segs + (bh * a.nseg + seg) * a.Kd * a.Vd;
-#pragma unroll
-        for (int j = 0; j < KD / 16; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (state_at(j, i) < a.Kd) o[state_at(j, i) * a.Vd + v] = st[j][i];
+        float* p = a.parts + (bh * a.nparts + seg) * per;
+        each_of_state(false, [&](float x, int i) MSS_INLINED { return p[i] = x; });
     } else {
-        for (int64_t t = (from > len ? from : len) + r16; t < to; t += 16) {  // past the end
-            auto* o = static_cast<typename OUT::storage*>(a.out) + ((b * a.L + t) * a.H + h) * a.Vd + v0 + 4 * g;
-            if (sizeof(typename OUT::storage) == 2) *reinterpret_cast<uint2*>(o) = make_uint2(0, 0);
-            else *reinterpret_cast<f32x4*>(o) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int64_t t = (from > len ? from : len) + r16; t < to && sub == 0; t += 16) {  // past the end
+            char* p = static_cast<char*>(a.out) + (((b * a.L + t) * a.outs + o_head) * a.Vd + v0 + 4 * g) * static_cast<int64_t>(sizeof(O));
+            if (sizeof(O) == 2) *reinterpret_cast<uint2*>(p) = make_uint2(0, 0);
+            else *reinterpret_cast<f32x4*>(p) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         if (a.last && seg == a.nseg - 1) {
             // walked backwards, the state is that of the first step: the one before it is a step further
-            const float f = a.back && len > 0 ? power(1) : 1.0f;
-            float* o = a.last + bh * a.Kd * a.Vd;
-#pragma unroll
-            for (int j = 0; j < KD / 16; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int k = state_at(j, i);
-                    if (k < a.Kd) o[a.turned ? v * a.Kd + k : k * a.Vd + v] = st[j][i] * f;
-                }
+            const float f = back && len > 0 ? power(1) : 1.0f;
+            float* p = a.last + bh * per;
+            each_of_state(a.turned, [&](float x, int i) MSS_INLINED { return p[i] = x * f; });
         }
     }
 }
 
-// The states that enter the segments, from what each of them adds: a thread per element, in place.
-__global__ __launch_bounds__(256) void attention_join_kernel(AArgs a) {
-    const int64_t per = static_cast<int64_t>(a.Kd) * a.Vd, all = a.Bt * a.H * per;
-    for (int64_t e = blockIdx.x * 256ll + threadIdx.x; e < all; e += gridDim.x * 256ll) {
-        const int64_t bh = e / per, x = e % per, b = bh / a.H;
-        const int64_t len = a.lens ? (a.lens[b] < 0 ? 0 : a.lens[b] < a.L ? a.lens[b] : a.L) : a.L;
-        const float rate = fminf(fmaxf(a.rate[bh % a.H], 0.0f), kMostRate);
-        float s = 0.0f;
-        if (a.init) s = a.init[bh * per + (a.turned ? x % a.Vd * a.Kd + x / a.Vd : x)];
-        float* o = a.segs + bh * a.nseg * per + x;
-        for (int seg = 0; seg < a.nseg; ++seg) {
-            const float adds = seg + 1 < a.nseg ? o[seg * per] : 0.0f;
-            o[seg * per] = s;
-            int64_t n = len - seg * a.seg_steps;
-            n = n < 0 ? 0 : n < a.seg_steps ? n : a.seg_steps;
-            if (n > 0 && seg == 0 && a.back) --n;
-            s = fmaf(s, expm1f(-rate * static_cast<float>(n)), s) + adds;
+// The states that enter the segments but the first, from what the parts add, in place (in the last part of the segment
+// before): a block per (batch, head) and 256 elements.
+__global__ __launch_bounds__(256) void attention_join_kernel(Walks all, int blocks) {
+    const AArgs& a = all.w[blockIdx.x / all.each];
+    const int64_t block = blockIdx.x % all.each, bh = block / blocks, b = bh / a.H;
+    const int per = a.Kd * a.Vd, x = static_cast<int>(block % blocks) * 256 + threadIdx.x;
+    if (x >= per) return;
+    const int64_t len = a.lens ? (a.lens[b] < 0 ? 0 : a.lens[b] < a.L ? a.lens[b] : a.L) : a.L;
+    const float rate = fminf(fmaxf(a.rate[bh % a.H], 0.0f), kMostRate);
+    float s = 0.0f;
+    if (a.init) s = a.init[bh * per + (a.turned ? x % a.Vd * a.Kd + x / a.Vd : x)];
+    float* o = a.parts + bh * a.nparts * per + x;
+    constexpr int G = 16;  // on their way at once
+    for (int i0 = 0; i0 < a.nparts; i0 += G) {
+        float adds[G];
+#pragma unroll
+        for (int i = 0; i < G; ++i) adds[i] = o[static_cast<int64_t>(i0 + i < a.nparts ? i0 + i : i0) * per];
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            if (i0 + i >= a.nparts) break;
+            s = fmaf(s, part_decay(a, rate, len, i0 + i), s) + adds[i];
+            // (parts before the last of a segment hold what no one reads; the segment's last gives the next one's state)
+            if ((i0 + i + 1) % a.cuts == 0) o[static_cast<int64_t>(i0 + i) * per] = s;
         }
     }
 }
@@ -461,65 +632,163 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
     }
 }
 
-// Segments, and steps of each: blocks for every CU twice over, but none of under 256 steps (each re-reads its keys and
-// values).
-void plan_segments(int64_t Bt, int64_t L, int H, int Vd, int* nseg, int64_t* steps) {
-    const int64_t blocks = Bt * H * ((Vd + kVTile - 1) / kVTile);
-    const int64_t most = std::max<int64_t>(1, L / 256);
-    const int64_t n = std::min(most, std::max<int64_t>(1, 512 / std::max<int64_t>(1, blocks)));
-    *steps = std::max<int64_t>(64, ((L + n - 1) / n + 63) / 64 * 64);
-    *nseg = static_cast<int>(std::max<int64_t>(1, (L + *steps - 1) / *steps));
+// How a sequence is cut.  A block walks a segment in about the same time for every 64 steps (4 us with 128 keys), and a CU
+// with more than one block takes longer by what they share: measured for c blocks of eight waves 0.9 c, for four waves
+// 0.1 + 0.7 c, for 16 waves, which do not fit twice, 1.3 c.  The start of a segment is worth one such time.  More segments
+// fill the CUs better but need the states between them: a pass over keys and values at 0.6 (eight waves) or 0.4 (four) of
+// the walk, and a launch.  That pass, whose blocks wait for nothing, is cut further, into parts of 128 steps or more, up
+// to two blocks for every CU.
+// Times by the number of segments, the one that is taken in brackets: 4 x 2048 x 32 heads of 128 x 128 bf16, 1 to 4: 142,
+// [118], 119, 129 us; 3 x 1531 x 12 heads of 64 x 96 f32, 4, 6, 8, 16: 68, [60], 79, 65; 1 x 2048 x 32 heads of 128 x 128
+// bf16 with shared keys and values, 4, 6, 8, 16: 73, 64, [59], 61.
+struct Plan {
+    int nseg, nparts, cuts;
+    int64_t part_steps;
+};
+// blocks: of each segment; heads: whose states are wanted; waves: of a block, of one of those that make states
+Plan plan_segments(int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
+    const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64);
+    int64_t best = 0, segment = steps64;
+    for (int64_t n = 1; n <= std::min<int64_t>(64, steps64 / 2 + 1); ++n) {
+        const int64_t each = (steps64 + n - 1) / n, segs = (steps64 + each - 1) / each;  // of 64 steps, and how many there are
+        const int64_t c = (blocks * segs + 255) / 256;
+        const int64_t per = waves == 16 ? 13 * c : std::max<int64_t>(10, waves == 8 ? 9 * c : 1 + 7 * c);
+        int64_t cost = per * (each + 1);
+        if (segs > 1) cost += (state_waves == 8 ? 6 : 4) * heads * (segs - 1) * each / 256 + 15;
+        if (n == 1 || cost < best) best = cost, segment = each;
+    }
+    Plan p;
+    p.nseg = static_cast<int>((steps64 + segment - 1) / segment);
+    p.cuts = 1;
+    while (p.nseg > 1 && segment % (2 * p.cuts) == 0 && segment / (2 * p.cuts) >= 2 && heads * (p.nseg - 1) * p.cuts < 512)
+        p.cuts *= 2;
+    p.part_steps = segment * 64 / p.cuts;
+    p.nparts = (p.nseg - 1) * p.cuts;
+    return p;
+}
+// Columns of a block.
+int columns(int Vd) { return Vd > 64 ? 128 : 64; }
+// Heads of a group that a block does: 16 waves of bf16's kernels find room on a CU, eight of fp32's smallest.
+constexpr int heads_at_once(bool bf16, int KD, int NW) { return bf16 ? 16 / NW : KD == 64 && NW == 4 ? 2 : 1; }
+
+Plan plan_walks(bool bf16, int64_t Bt, int64_t L, int H, int outs, int each, int Kd, int Vd, int count) {
+    const int waves = columns(Vd) / 16;
+    return plan_segments(Bt * outs * count, Bt * H * count,
+                         each > 1 ? waves * heads_at_once(bf16, Kd <= 64 ? 64 : 128, waves) : waves, waves, L);
 }
 
-template <class E, class OUT, int KD>
-void walk_kd(const AArgs& a, hipStream_t s) {
-    const int64_t heads = a.Bt * a.H * ((a.Vd + kVTile - 1) / kVTile);
-    if (a.nseg > 1) {
-        attention_kernel<E, E, KD, true><<<dim3(static_cast<unsigned>(heads * (a.nseg - 1))), dim3(64 * kWaves), 0, s>>>(a);
-        attention_join_kernel<<<dim3(blocks_for(a.Bt * a.H * a.Kd * a.Vd, 256)), dim3(256), 0, s>>>(a);
+template <class E, class OUT, int KD, int NW>
+void walk_waves(Walks& w, int count, hipStream_t s) {
+    constexpr int SUB = heads_at_once(Form<E>::NP == 1, KD, NW);
+    const AArgs& a = w.w[0];
+    const dim3 block(64 * NW);
+    const auto grid = [&](int64_t each) {
+        w.each = each;
+        return dim3(static_cast<unsigned>(each * count));
+    };
+    if (a.nparts > 0) {
+        attention_kernel<E, E, KD, NW, 1, true><<<grid(a.Bt * a.H * a.nparts), block, 0, s>>>(w);
+        const int blocks = (a.Kd * a.Vd + 255) / 256;
+        if (a.nparts > kFold) attention_join_kernel<<<grid(a.Bt * a.H * blocks), dim3(256), 0, s>>>(w, blocks);
     }
-    attention_kernel<E, OUT, KD, false><<<dim3(static_cast<unsigned>(heads * a.nseg)), dim3(64 * kWaves), 0, s>>>(a);
+    const int64_t blocks = a.Bt * a.outs * a.nseg;
+    if constexpr (SUB > 1) {
+        if (a.each > 1) {
+            attention_kernel<E, OUT, KD, NW, SUB, false><<<grid(blocks), dim3(64 * NW * SUB), 0, s>>>(w);
+            return;
+        }
+    }
+    attention_kernel<E, OUT, KD, NW, 1, false><<<grid(blocks), block, 0, s>>>(w);
 }
+// Walks of the same sizes and type of outputs, side by side; their states in scratch.
 template <class E, class OUT>
-void walk(const AArgs& a, hipStream_t s) {
-    if (a.Kd <= 64) walk_kd<E, OUT, 64>(a, s);
-    else walk_kd<E, OUT, 128>(a, s);
+void walk(Walks& w, int count, float* scratch, hipStream_t s) {
+    const Plan p = plan_walks(Form<E>::NP == 1, w.w[0].Bt, w.w[0].L, w.w[0].H, w.w[0].outs, w.w[0].each, w.w[0].Kd,
+                              w.w[0].Vd, count);
+    for (int i = 0; i < count; ++i) {
+        AArgs& a = w.w[i];
+        a.nseg = p.nseg; a.nparts = p.nparts; a.cuts = p.cuts; a.part_steps = p.part_steps;
+        a.parts = scratch + i * a.Bt * a.H * p.nparts * a.Kd * a.Vd;
+    }
+    const bool wide = columns(w.w[0].Vd) == 128;
+    if (w.w[0].Kd <= 64) {
+        if (wide) walk_waves<E, OUT, 64, 8>(w, count, s);
+        else walk_waves<E, OUT, 64, 4>(w, count, s);
+    } else {
+        if (wide) walk_waves<E, OUT, 128, 8>(w, count, s);
+        else walk_waves<E, OUT, 128, 4>(w, count, s);
+    }
 }
+
+// The backward's walks: of what sizes, from and to where.  Those of equal sizes whose outputs are alike go in one launch.
+struct Role {
+    Rows q, k, v;
+    void* out;
+    int heads, Kd, Vd;  // heads of out
+    bool back, turned;
+    int each, outs;     // as the kernel takes them
+    int sums;           // outputs of a group that are still to be added up (1: none)
+};
+struct Roles {
+    Role r[kMostWalks];
+    int first[kMostWalks + 1], count;  // launches
+};
+Roles roles_of(const AttnLaunch& l) {
+    const Rows q{l.q, l.Hq}, k{l.k, l.Hk}, v{l.v, l.Hv}, d{l.dout, l.H};
+    Roles o{{{d, v, k, l.dq, l.Hq, l.V, l.K, false, true, 1, l.H, 1},
+             {v, d, q, l.dk, l.Hk, l.V, l.K, true, true, 1, l.H, 1},
+             {k, q, d, l.dv, l.Hv, l.K, l.V, true, false, 1, l.H, 1}}, {0, 1, 2, 3}, 0};
+    for (int i = 0; i < kMostWalks; ++i) {
+        Role& a = o.r[i];
+        if (a.heads < l.H) {
+            const int sub = heads_at_once(l.bf16, a.Kd <= 64 ? 64 : 128, columns(a.Vd) / 16), each = l.H / a.heads;
+            a.sums = sub > 1 ? (each + sub - 1) / sub : each;
+            a.each = sub > 1 ? each : 1;
+            a.outs = a.heads * a.sums;
+        }
+        const Role& b = o.r[i > 0 ? i - 1 : 0];
+        if (i == 0 || a.Kd != b.Kd || a.Vd != b.Vd || a.each != b.each || a.sums != b.sums || a.outs != b.outs)
+            o.first[o.count++] = i;
+    }
+    o.first[o.count] = kMostWalks;
+    return o;
+}
+// Floats of scratch of a launch's states, and of a walk's sums before they are added up.
+int64_t states_of(const AttnLaunch& l, const Role& r, int count) {
+    return count * l.Bt * l.H * l.K * l.V *
+           plan_walks(l.bf16, l.Bt, l.L, l.H, r.outs, r.each, r.Kd, r.Vd, count).nparts;
+}
+int64_t sums_of(const AttnLaunch& l, const Role& r) { return r.sums > 1 ? l.Bt * l.L * r.outs * r.Vd : 0; }
 
 template <class E>
 void backward(const AttnLaunch& l, hipStream_t s) {
-    // (queries, keys, values) of each walk; K x V states are read the other way round where the roles of K and V are
-    const Rows q{l.q, l.Hq}, k{l.k, l.Hk}, v{l.v, l.Hv}, d{l.dout, l.H};
-    struct Walk {
-        Rows q, k, v;
-        void* out;
-        int heads, Kd, Vd;
-        bool back, turned;
-    };
-    const Walk walks[3] = {{d, v, k, l.dq, l.Hq, l.V, l.K, false, true},
-                           {v, d, q, l.dk, l.Hk, l.V, l.K, true, true},
-                           {k, q, d, l.dv, l.Hv, l.K, l.V, true, false}};
-    for (const Walk& w : walks) {
-        AArgs a{};
-        a.q = w.q; a.k = w.k; a.v = w.v; a.rate = l.rate; a.lens = l.lens; a.Bt = l.Bt; a.L = l.L; a.H = l.H;
-        a.Kd = w.Kd; a.Vd = w.Vd; a.back = w.back;
-        a.turned = w.turned;
-        a.init = w.back ? l.dlast : l.h0;
-        a.last = w.back && !w.turned ? l.dh0 : nullptr;
-        a.s_add = w.back ? l.scale : 1.0f;
-        a.s_out = w.back ? 1.0f : l.scale;
-        plan_segments(l.Bt, l.L, l.H, w.Vd, &a.nseg, &a.seg_steps);
-        a.segs = l.scratch;
-        if (w.heads == l.H) {
-            a.out = w.out;
-            walk<E, E>(a, s);
-        } else {
-            const int64_t states = a.nseg > 1 ? l.Bt * l.H * a.nseg * l.K * l.V : 0;
-            float* part = l.scratch + states;
-            a.out = part;
-            walk<E, F32>(a, s);
-            const int64_t n = l.Bt * l.L * w.heads * w.Vd / 4;
-            if (n) attention_groups_kernel<E><<<dim3(blocks_for(n, 256)), dim3(256), 0, s>>>(part, w.out, n, l.H / w.heads, w.Vd);
+    const Roles o = roles_of(l);
+    for (int n = 0; n < o.count; ++n) {
+        const int from = o.first[n], count = o.first[n + 1] - from;
+        Walks w{};
+        float* sums = l.scratch + states_of(l, o.r[from], count);
+        for (int i = 0; i < count; ++i) {
+            const Role& r = o.r[from + i];
+            AArgs& a = w.w[i];
+            a.q = r.q; a.k = r.k; a.v = r.v; a.rate = l.rate; a.lens = l.lens; a.Bt = l.Bt; a.L = l.L; a.H = l.H;
+            a.Kd = r.Kd; a.Vd = r.Vd; a.back = r.back; a.turned = r.turned; a.each = r.each; a.outs = r.outs;
+            a.init = r.back ? l.dlast : l.h0;
+            a.last = r.back && !r.turned ? l.dh0 : nullptr;
+            a.s_add = r.back ? l.scale : 1.0f;
+            a.s_out = r.back ? 1.0f : l.scale;
+            a.out = r.sums == 1 ? r.out : sums + i * sums_of(l, r);
+        }
+        if (o.r[from].sums == 1) {
+            walk<E, E>(w, count, l.scratch, s);
+            continue;
+        }
+        walk<E, F32>(w, count, l.scratch, s);
+        for (int i = 0; i < count; ++i) {
+            const Role& r = o.r[from + i];
+            const int64_t all = l.Bt * l.L * r.heads * r.Vd / 4;
+            if (all)
+                attention_groups_kernel<E><<<dim3(blocks_for(all, 256)), dim3(256), 0, s>>>(
+                    static_cast<const float*>(w.w[i].out), r.out, all, r.sums, r.Vd);
         }
     }
 }
@@ -527,32 +796,30 @@ void backward(const AttnLaunch& l, hipStream_t s) {
 }  // namespace
 
 int64_t attn_fwd_scratch(int64_t Bt, int64_t L, int H, int K, int V) {
-    int nseg;
-    int64_t steps;
-    plan_segments(Bt, L, H, V, &nseg, &steps);
-    return nseg > 1 ? Bt * H * nseg * K * V : 0;
+    return Bt * H * plan_walks(true, Bt, L, H, H, 1, K, V, 1).nparts * K * V;
 }
 
-int64_t attn_bwd_scratch(int64_t Bt, int64_t L, int H, int Hq, int Hk, int Hv, int K, int V) {
+int64_t attn_bwd_scratch(int64_t Bt, int64_t L, int H, int Hq, int Hk, int Hv, int K, int V, bool bf16) {
+    AttnLaunch l{};
+    l.bf16 = bf16;
+    l.Bt = Bt; l.L = L; l.H = H; l.Hq = Hq; l.Hk = Hk; l.Hv = Hv; l.K = K; l.V = V;
+    const Roles o = roles_of(l);
     int64_t most = 0;
-    for (const auto& w : {std::pair<int, int>{Hq, K}, {Hk, K}, {Hv, V}}) {
-        int nseg;
-        int64_t steps;
-        plan_segments(Bt, L, H, w.second, &nseg, &steps);
-        const int64_t n = (nseg > 1 ? Bt * H * nseg * K * V : 0) + (w.first < H ? Bt * L * H * w.second : 0);
-        most = std::max(most, n);
+    for (int n = 0; n < o.count; ++n) {
+        const int from = o.first[n], count = o.first[n + 1] - from;
+        most = std::max(most, states_of(l, o.r[from], count) + count * sums_of(l, o.r[from]));
     }
     return most;
 }
 
 hipError_t launch_attn_fwd(const AttnLaunch& l, hipStream_t s) {
-    AArgs a{};
+    Walks w{};
+    AArgs& a = w.w[0];
     a.q = {l.q, l.Hq}; a.k = {l.k, l.Hk}; a.v = {l.v, l.Hv}; a.rate = l.rate; a.lens = l.lens; a.init = l.h0;
-    a.last = l.last_state; a.segs = l.scratch; a.out = l.out; a.Bt = l.Bt; a.L = l.L; a.H = l.H; a.Kd = l.K; a.Vd = l.V;
-    a.s_add = 1.0f; a.s_out = l.scale;
-    plan_segments(l.Bt, l.L, l.H, l.V, &a.nseg, &a.seg_steps);
-    if (l.bf16) walk<BF16, BF16>(a, s);
-    else walk<F32, F32>(a, s);
+    a.last = l.last_state; a.out = l.out; a.Bt = l.Bt; a.L = l.L; a.H = l.H; a.Kd = l.K; a.Vd = l.V;
+    a.s_add = 1.0f; a.s_out = l.scale; a.each = 1; a.outs = l.H;
+    if (l.bf16) walk<BF16, BF16>(w, 1, l.scratch, s);
+    else walk<F32, F32>(w, 1, l.scratch, s);
     return hipGetLastError();
 }
 

@@ -70,11 +70,11 @@ def attn_args(dt=MSS_BF16):
                 last_state=T([B, H, K, V]), scratch=T([1 << 20]))
 
 
-def attn_bwd_args(dt=MSS_BF16):
-    return dict(q=T([B, L, Q, K], dt), k=T([B, L, KH, K], dt), v=T([B, L, VH, V], dt), rate=T([H]), scale=0.5,
-                initial_state=T([B, H, K, V]), seq_lens=T([B], MSS_I32), dout=T([B, L, H, V], dt),
-                dlast_state=T([B, H, K, V]), dq=T([B, L, Q, K], dt), dk=T([B, L, KH, K], dt), dv=T([B, L, VH, V], dt),
-                dinitial_state=T([B, H, K, V]), scratch=T([1 << 20]))
+def attn_bwd_args(dt=MSS_BF16):  # eight heads to a query: their gradients meet in scratch
+    return dict(q=T([B, L, Q, K], dt), k=T([B, L, KH, K], dt), v=T([B, L, VH, V], dt), rate=T([2 * H]), scale=0.5,
+                initial_state=T([B, 2 * H, K, V]), seq_lens=T([B], MSS_I32), dout=T([B, L, 2 * H, V], dt),
+                dlast_state=T([B, 2 * H, K, V]), dq=T([B, L, Q, K], dt), dk=T([B, L, KH, K], dt), dv=T([B, L, VH, V], dt),
+                dinitial_state=T([B, 2 * H, K, V]), scratch=T([1 << 20]))
 
 
 def step_args(dt=MSS_BF16):
