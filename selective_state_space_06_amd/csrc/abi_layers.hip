@@ -317,7 +317,6 @@ int mss_token_logprobs_fwd(const mss_tensor_t* logits, const mss_tensor_t* token
         a.scratch = ptr<float>(scratch);
         a.R = R; a.V = V; a.K = static_cast<int>(K);
         a.bf16 = logits->dtype == MSS_BF16;
-        a.vec_ok = whole_vectors(V, logits->dtype, {logits});
         if (R == 0) return MSS_OK;
         return status(mss::launch_logprob_fwd(a, static_cast<hipStream_t>(stream)));
     } catch (...) {

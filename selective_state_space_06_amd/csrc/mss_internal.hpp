@@ -349,7 +349,7 @@ struct LogprobLaunch {
     float* scratch;
     int64_t R, V;
     int K;                       // 0: no alternatives
-    bool bf16, vec_ok;
+    bool bf16;
 };
 struct LogprobBwdLaunch {
     const void* logits;

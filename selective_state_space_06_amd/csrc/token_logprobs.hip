@@ -3,10 +3,17 @@
 //
 // Forward: with m the greatest logit, s = sum e^(x - m) and t = sum e^(x - m) (x - m), the log probability of a token
 // is (x_token - m) - log s and the entropy log s - t / s.  One pass: every lane keeps its own m, s and t, rescaled
-// when its m rises, and a wave its list of the k greatest logits (top_lists.hpp); lanes, waves and, where a row is
-// cut into slices, blocks are joined in 64 bits.  Backward: with p = e^(x - m) / s,
+// when its m rises; lanes, waves and, where a row is cut into slices, blocks are joined in 64 bits.  The alternatives come
+// from the lanes' greatest logits: they bound the k-th greatest of the block from below, so that only the few lanes whose
+// own greatest is not under the bound have their tiles read again (from the L2 cache).  Lists of 64-bit keys are merged
+// pairwise.  Backward: with p = e^(x - m) / s,
 //     dx_v = g (1[v = token] - p_v) - h p_v (log p_v + entropy),
-// one pass over the logits from the row's m, 1 / s and entropy - log s.  Both are bound by memory.
+// one pass over the logits from the row's m, 1 / s and entropy - log s.
+//
+// Both are bound by memory where there is enough of it: 4096 x 50280 bf16 79 us forward (5.2 TB/s), 151 backward
+// (5.5 TB/s).  A batch of 128 x 128007 bf16 takes 13 us without alternatives (2.5 TB/s; 6.4 at the rate of a copy, the rest is the
+// ends of two launches), 18 with 5 of them and 23 with 20; as lists kept by every wave along its way 14, 23 and 39.  One row of
+// 50277 f32 with 20 alternatives takes 15 us, mostly latencies in a row: launches, loads, merges.
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -66,20 +73,45 @@ __device__ __forceinline__ void join_lanes(Sums& v, int count) {
     v.t = __shfl(v.t, 0);
 }
 
-// A row's outputs by one wave; `key`: lane j's alternative.
+// The k greatest of two sorted lists, `other` held the other way round (entry j in lane size - 1 - j): the greater of each
+// pair of entries, which rises and falls, sorted by comparing lanes ever closer to each other.  size: list_size(k).
+__device__ __forceinline__ int list_size(int k) { return k > 1 ? 1 << (32 - __builtin_clz(k - 1)) : 1; }
+__device__ __forceinline__ uint64_t merge_two(uint64_t key, uint64_t other, int size, int lane) {
+    key = other > key ? other : key;
+    for (int x = size / 2; x > 0; x >>= 1) {
+        const uint64_t o = __shfl_xor(key, x);
+        key = (o > key) == ((lane & x) == 0) ? o : key;
+    }
+    return key;
+}
+// Joins the lists of W waves into wave 0's (lanes from k on hold kNone).  Every wave comes here.
+template <int W>
+__device__ __forceinline__ void join_lists(uint64_t* all, uint64_t& key, int k, int wave, int lane) {
+    const int size = list_size(k);
+    for (int w = W / 2; w > 0; w >>= 1) {
+        if (wave >= w && wave < 2 * w && lane < size) all[wave * 64 + size - 1 - lane] = key;
+        __syncthreads();
+        if (wave < w) key = merge_two(key, lane < size ? all[(wave + w) * 64 + lane] : kNone, size, lane);
+        if (lane >= k) key = kNone;
+    }
+}
+
+// The logit of the row's token, read long before it is used.
 template <class E>
-__device__ __forceinline__ void finish_row(const LArgs& a, int64_t row, const Sums& v, uint64_t key, int lane) {
+__device__ __forceinline__ float logit_of_token(const LArgs& a, int64_t row) {
+    const int64_t token = a.tokens[row];
+    return E::load1(a.logits, row * a.V + (token >= 0 && token < a.V ? token : 0));
+}
+
+// A row's outputs by one wave; `given`: its token's logit; `key`: lane j's alternative.
+__device__ __forceinline__ void finish_row(const LArgs& a, int64_t row, float given, const Sums& v, uint64_t key, int lane) {
     const bool dead = v.s == 0.0;  // every logit is -inf
     const double ls = dead ? 0.0 : log(v.s);
     const float entropy = dead ? 0.0f : static_cast<float>(ls - v.t / v.s);
     if (lane == 0) {
         const int64_t token = a.tokens[row];
-        float lp = 0.0f;
-        if (token >= 0 && token < a.V) {
-            const float x = E::load1(a.logits, row * a.V + token);
-            lp = dead ? -INFINITY : static_cast<float>((static_cast<double>(x) - v.m) - ls);
-        }
-        a.logprobs[row] = lp;
+        const bool in = token >= 0 && token < a.V;
+        a.logprobs[row] = !in ? 0.0f : dead ? -INFINITY : static_cast<float>((static_cast<double>(given) - v.m) - ls);
         if (a.entropy) a.entropy[row] = entropy;
         if (a.saved) {
             float* o = a.saved + row * 3;
@@ -96,42 +128,41 @@ __device__ __forceinline__ void finish_row(const LArgs& a, int64_t row, const Su
     }
 }
 
-// One block per (row, slice of the vocabulary), its waves on successive parts of the slice, each with two tiles on
-// their way.  VEC: rows are whole aligned 16-byte vectors.
-constexpr int kWaves = 8;
+// One block per (row, slice of the vocabulary), its waves on successive tiles in turn, kAhead of them on their way, by
+// loads that are not branched around (past the end they give 0).  Which lane takes which logit does not depend on where the
+// row lies, so that equal rows have equal results: rows of any alignment are loaded as they are (4096 x 50277 bf16: 101 us
+// with branches, 92 without).
+constexpr int kWaves = 4, kAhead = 2;
 
-template <class E, bool VEC, bool TOP>
+template <class E, bool TOP>
 __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
     using S = typename E::storage;
-    __shared__ uint64_t all[TOP ? kWaves * kBeamMost : 1];
+    constexpr int ES = sizeof(S);
+    __shared__ uint64_t all[TOP ? kWaves * 64 : 1];
     __shared__ double all_s[kWaves], all_t[kWaves];
     __shared__ float all_m[kWaves];
+    __shared__ uint32_t bars[2][kWaves];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
-    const int64_t works = a.R * a.slices, tiles = (a.V + kTile - 1) / kTile;
+    const int64_t works = a.R * a.slices;
     for (int64_t g = blockIdx.x; g < works; g += gridDim.x) {
-        const int64_t row = g / a.slices, from = g % a.slices * a.tiles;
-        const int64_t to = from + a.tiles < tiles ? from + a.tiles : tiles;
-        const int64_t per = (to - from + kWaves - 1) / kWaves;
-        const int64_t lo = from + wave * per, hi = lo + per < to ? lo + per : to;  // this wave's tiles
+        const int64_t row = g / a.slices;
+        const int slice = static_cast<int>(g % a.slices);
         const S* p = static_cast<const S*>(a.logits) + row * a.V;
-        List list;
+        const int64_t tiles = (a.V + kTile - 1) / kTile, from = slice * a.tiles;
+        const int64_t to = from + a.tiles < tiles ? from + a.tiles : tiles;
         float m = -INFINITY, s = 0.0f, t = 0.0f;
-        Raw<E> raw[2] = {};
+        Raw<E> raw[kAhead];
         const auto load = [&](int64_t k, Raw<E>& r) MSS_INLINED {
-            load8<E, VEC>(p + k * kTile, a.V, clamp_tile(a.V - k * kTile), lane, r);
-        };
-        const auto tile = [&](int64_t k, Raw<E>& r, auto first) MSS_INLINED {
-            const int rem = clamp_tile(a.V - k * kTile);
-            settle8<E, VEC>(a.V, rem, lane, r);
-            float v[kE];
-            r.unpack(v);
-            if (k + 2 < hi) load(k + 2, r);
-            if (rem < kTile) {
+            const int rem = k < to ? clamp_tile(a.V - k * kTile) : 0;
+            const bool half = ES == 2 && rem & 1;  // the last logit is half of a word, which a buffer does not hold
+            const auto buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<S*>(p + k * kTile), 0, half ? 0 : rem * ES, 0x00027000);
 #pragma unroll
-                for (int e = 0; e < kE; ++e)
-                    if (lane * kE + e >= rem) v[e] = -INFINITY;
-            }
+            for (int i = 0; i < kE / E::kPerVec; ++i)
+                r.q[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(buffer, lane * kE * ES + 16 * i, 0, 0));
+            if (half) load8<E, false>(p + k * kTile, a.V, rem, lane, r);
+        };
+        const auto take = [&](const float* v) MSS_INLINED {
             float best = v[0];
 #pragma unroll
             for (int e = 1; e < kE; ++e) best = fmaxf(best, v[e]);
@@ -151,44 +182,98 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
             }
             s += ss;
             t += tt;
-            if constexpr (TOP) {
-                if (ss != ss) {  // a NaN logit, which is no alternative (or one of +inf)
-#pragma unroll
-                    for (int e = 0; e < kE; ++e) v[e] = v[e] == v[e] ? v[e] : -INFINITY;
-                }
-                const uint32_t most = order_of(best == best ? best : -INFINITY);
-                uint32_t bar = static_cast<uint32_t>(list.last >> 32);  // nothing below it is among the k best
-                if (decltype(first)::value) {
-                    uint32_t cut = 0;
-#pragma unroll
-                    for (int bit = 31; bit >= 16; --bit) {
-                        const uint32_t c = cut | 1u << bit;
-                        if (__popcll(ballot(most >= c)) >= a.K) cut = c;
-                    }
-                    bar = cut > bar ? cut : bar;
-                }
-                if (ballot(most >= bar) == 0) return;
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const uint32_t o = order_of(v[e]);
-                    const uint64_t key = key_of(o, static_cast<int>(k * kTile) + lane * kE + e);
-                    uint64_t left = ballot((o >= bar) & (key > list.last));
-                    while (left) {
-                        list.insert(lane_of(key, first_of(left)), a.K, lane);
-                        left &= left - 1;
-                        left &= ballot(key > list.last);
-                    }
-                }
-            }
         };
-        if (lo < hi) {
-            load(lo, raw[0]);
-            if (lo + 1 < hi) load(lo + 1, raw[1]);
-            tile(lo, raw[0], True{});
-            for (int64_t k = lo + 1; k < hi; k += 2) {
-                tile(k, raw[1], False{});
-                if (k + 1 < hi) tile(k + 1, raw[0], False{});
+        const auto tile = [&](int64_t k, Raw<E>& r) MSS_INLINED {
+            const int rem = clamp_tile(a.V - k * kTile);
+            if (ES == 2 && rem & 1) settle8<E, false>(a.V, rem, lane, r);
+            float v[kE];
+            r.unpack(v);
+            load(k + kAhead * kWaves, r);
+            if (k >= to) return;
+            if (rem < kTile) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                    if (lane * kE + e >= rem) v[e] = -INFINITY;
             }
+            take(v);
+        };
+        const int64_t lo = from + wave;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) load(lo + i * kWaves, raw[i]);
+        const float given = a.slices == 1 && wave == 0 ? logit_of_token<E>(a, row) : 0.0f;
+        for (int64_t k = lo; k < to; k += kAhead * kWaves) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) tile(k + i * kWaves, raw[i]);
+        }
+        uint64_t key = kNone;
+        if constexpr (TOP) {
+            // the alternatives are at least as great as the k-th greatest of any wave's lanes, and as the least of the
+            // waves' (k / kWaves)-th greatest
+            const uint32_t most = order_of(m);
+            const int share = (a.K + kWaves - 1) / kWaves;
+            uint32_t kth = 0, part = 0;
+#pragma unroll
+            for (int bit = 31; bit >= 16; --bit) {
+                const uint32_t c = kth | 1u << bit, d = part | 1u << bit;
+                if (__popcll(ballot(most >= c)) >= a.K) kth = c;
+                if (__popcll(ballot(most >= d)) >= share) part = d;
+            }
+            if (lane == 0) bars[0][wave] = kth, bars[1][wave] = part;
+            __syncthreads();
+            uint32_t bar = kLeast;
+            {
+                uint32_t least = ~0u;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) {
+                    bar = bars[0][w] > bar ? bars[0][w] : bar;
+                    least = bars[1][w] < least ? bars[1][w] : least;
+                }
+                bar = least > bar ? least : bar;
+            }
+            List list;
+            const auto offer = [&](uint32_t o, int token) MSS_INLINED {
+                const uint64_t k = key_of(o, token);
+                uint64_t left = ballot((o >= bar) & (k > list.last));
+                while (left) {
+                    list.insert(lane_of(k, first_of(left)), a.K, lane);
+                    left &= left - 1;
+                    left &= ballot(k > list.last);
+                }
+            };
+            // the tiles of the lanes that have such logits again, 64 vectors of them at a time
+            const int mine = lo < to ? static_cast<int>((to - lo + kWaves - 1) / kWaves) : 0;
+            int lg = 0;
+            while (lg < 6 && 1 << lg < mine) ++lg;
+            const int first_token = static_cast<int>(lo * kTile);
+            uint64_t hot = ballot(mine > 0 && most >= bar);
+            while (hot) {
+                const int rank = __popcll(hot & ((1ull << lane) - 1)), count = __popcll(hot);
+                const int order = __builtin_amdgcn_ds_permute(4 * (hot >> lane & 1 ? rank : count + lane - rank), lane);
+                const int src = __shfl(order, lane >> lg);
+                for (int base = 0; base < mine; base += 64) {
+                    const int i = base + (lane & ((1 << lg) - 1));
+                    const int64_t at = (lo + static_cast<int64_t>(i) * kWaves) * kTile + src * kE;
+                    const bool in = lane >> lg < count && i < mine;
+                    const int n = !in || at >= a.V ? 0 : a.V - at < kE ? static_cast<int>(a.V - at) : kE;  // of this lane's
+                    float v[kE];
+                    if (n == kE) {
+                        Raw<E> r;
+                        __builtin_memcpy(r.q, p + at, sizeof(r.q));
+                        r.unpack(v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < kE; ++e) v[e] = e < n ? E::load1(p, at + e) : 0.0f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) v[e] = e < n && v[e] == v[e] ? v[e] : -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < kE; ++e) offer(order_of(v[e]), static_cast<int>(at) + e);
+                }
+                // those that were not taken, if they still can be among the k best
+                for (int i = 0; i < 64 >> lg && hot; ++i) hot &= hot - 1;
+                hot &= ballot(key_of(most, first_token + lane * kE) > list.last);
+            }
+            if (lane < a.K) key = list.key;
         }
         Sums v{m, s, t};
         join_lanes(v, 64);
@@ -197,51 +282,71 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
             all_s[wave] = v.s;
             all_t[wave] = v.t;
         }
-        if (TOP && lane < a.K) all[wave * a.K + lane] = list.key;
-        __syncthreads();
+        if (TOP) join_lists<kWaves>(all, key, a.K, wave, lane);
+        else __syncthreads();
         if (wave == 0) {
             v = lane < kWaves ? Sums{all_m[lane], all_s[lane], all_t[lane]} : Sums{-INFINITY, 0.0, 0.0};
             join_lanes(v, kWaves);
-            uint64_t got = kNone;
-            if constexpr (TOP) got = merge_lists(all, kWaves, a.K, lane);
             if (a.slices == 1) {
-                finish_row<E>(a, row, v, got, lane);
+                finish_row(a, row, given, v, key, lane);
             } else {
                 if (lane == 0) {
                     a.part_m[g] = v.m;
                     a.part_s[g] = v.s;
                     a.part_t[g] = v.t;
                 }
-                if (lane < a.K) a.cand[g * a.K + lane] = got;
+                if (lane < a.K) a.cand[g * a.K + lane] = key;
             }
         }
         __syncthreads();
     }
 }
 
-// Joins the slices of a row, a wave each.  Shared memory: the lists.
+// Joins the slices of a row: a block of kWaves waves, of which each takes every kWaves-th list.
 template <class E>
-__global__ __launch_bounds__(64) void logprob_join_kernel(LArgs a) {
-    extern __shared__ uint64_t lists[];  // (slices, K)
-    const int lane = threadIdx.x;
+__global__ __launch_bounds__(64 * kWaves) void logprob_join_kernel(LArgs a) {
+    __shared__ uint64_t all[kWaves * 64];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x) {
-        for (int e = lane; e < a.slices * a.K; e += 64) lists[e] = a.cand[row * a.slices * a.K + e];
         Sums v{-INFINITY, 0.0, 0.0};
-        if (lane < a.slices) v = Sums{a.part_m[row * a.slices + lane], a.part_s[row * a.slices + lane],
-                                      a.part_t[row * a.slices + lane]};
-        __syncthreads();
-        join_lanes(v, 64);
-        uint64_t got = kNone;
-        if (a.K > 0) got = merge_lists(lists, a.slices, a.K, lane);
-        finish_row<E>(a, row, v, got, lane);
+        float given = 0.0f;
+        if (wave == 0) {
+            given = logit_of_token<E>(a, row);
+            if (lane < a.slices) v = Sums{a.part_m[row * a.slices + lane], a.part_s[row * a.slices + lane],
+                                          a.part_t[row * a.slices + lane]};
+        }
+        uint64_t key = kNone;
+        if (a.K > 0) {
+            const int size = list_size(a.K), j = size - 1 - lane;
+            const uint64_t* lists = a.cand + row * a.slices * a.K + j;
+            constexpr int G = 4;  // lists on their way
+            for (int i0 = wave; i0 < a.slices; i0 += G * kWaves) {
+                uint64_t other[G];
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    const int l = i0 + i * kWaves;
+                    other[i] = l < a.slices && j >= 0 && j < a.K ? lists[l * a.K] : kNone;
+                }
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+                    if (i0 + i * kWaves < a.slices) key = merge_two(key, other[i], size, lane);
+            }
+            join_lists<kWaves>(all, key, a.K, wave, lane);
+        }
+        if (wave == 0) {
+            join_lanes(v, 64);
+            finish_row(a, row, given, v, key, lane);
+        }
         __syncthreads();
     }
 }
 
-// Blocks for every CU twice over, each wave with a tile; at most 64 slices.
+// Four blocks for every CU, each wave with a tile or more; at most 64 slices.  (128 x 128007 bf16 with 5 alternatives: two
+// blocks for every CU 19 us, four 18, eight 22; blocks of eight waves 19.)
 void plan_logprob(int64_t R, int64_t V, int64_t* per, int* slices) {
     const int64_t tiles = (V + kTile - 1) / kTile;
-    int64_t n = (512 + R - 1) / R;
+    int64_t n = (1024 + R - 1) / R;
     n = std::max<int64_t>(1, std::min({n, (tiles + kWaves - 1) / kWaves, int64_t{64}}));
     *per = (tiles + n - 1) / n;
     *slices = static_cast<int>((tiles + *per - 1) / *per);
@@ -332,20 +437,17 @@ hipError_t launch_logprob_fwd(const LogprobLaunch& l, hipStream_t s) {
     a.cand = reinterpret_cast<uint64_t*>(a.part_t + works);
     a.part_m = reinterpret_cast<float*>(a.cand + works * l.K);
     const dim3 grid(blocks_for(works, 1)), block(64 * kWaves);
-#define MSS_FWD(E, VEC)                                                     \
-    if (l.K) logprob_kernel<E, VEC, true><<<grid, block, 0, s>>>(a);        \
-    else logprob_kernel<E, VEC, false><<<grid, block, 0, s>>>(a)
     if (l.bf16) {
-        if (l.vec_ok) { MSS_FWD(BF16, true); } else { MSS_FWD(BF16, false); }
+        if (l.K) logprob_kernel<BF16, true><<<grid, block, 0, s>>>(a);
+        else logprob_kernel<BF16, false><<<grid, block, 0, s>>>(a);
     } else {
-        if (l.vec_ok) { MSS_FWD(F32, true); } else { MSS_FWD(F32, false); }
+        if (l.K) logprob_kernel<F32, true><<<grid, block, 0, s>>>(a);
+        else logprob_kernel<F32, false><<<grid, block, 0, s>>>(a);
     }
-#undef MSS_FWD
     if (a.slices > 1) {
-        const size_t lds = static_cast<size_t>(a.slices) * a.K * 8;
         const dim3 rows(blocks_for(l.R, 1));
-        if (l.bf16) logprob_join_kernel<BF16><<<rows, dim3(64), lds, s>>>(a);
-        else logprob_join_kernel<F32><<<rows, dim3(64), lds, s>>>(a);
+        if (l.bf16) logprob_join_kernel<BF16><<<rows, block, 0, s>>>(a);
+        else logprob_join_kernel<F32><<<rows, block, 0, s>>>(a);
     }
     return hipGetLastError();
 }

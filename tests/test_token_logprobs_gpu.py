@@ -206,3 +206,36 @@ def test_graph_side_stream_and_autograd(mss):
     mss.TokenLogprobsFunction.apply(leaf2, t)[0].mean().backward()  # a loss without the entropy
     mean = torch.full_like(g, 1 / 9)
     assert torch.equal(leaf2.grad, mss.token_logprobs_bwd(x, t, mss.token_logprobs_save(x, t)[2], mean, torch.zeros_like(g)))
+
+
+def test_alternatives_of_many_equal_logits_and_at_the_ends(mss):
+    """Rows whose lanes all hold the k-th greatest logit, and whose alternatives are their first and last tokens."""
+    rng = np.random.default_rng(31)
+    for V in (9, 517, 4099, 20001):
+        x = np.zeros((5, V), dtype=np.float32)
+        x[1] = rng.integers(0, 3, V)
+        x[2, -5:] = np.arange(5) + 1.0
+        x[2, :3] = 9.0
+        x[3] = np.arange(V, dtype=np.float32) / V
+        x[4] = -np.arange(V, dtype=np.float32) / V
+        c = dict(x=round_to_bf16(x), t=np.array([0, 1, V - 1, V // 2, 0], dtype=np.int32), g=np.ones(5, np.float32),
+                 h=np.ones(5, np.float32), dtype="bf16")
+        for top in (1, 7, 64):
+            check(mss, c, top=min(top, V))
+
+
+def test_alternatives_of_long_rows_in_one_block(mss):
+    """More rows than are cut, of more tiles to a wave than are read again at once; in distinct and in equal logits."""
+    import torch
+    R, V, k = 1030, 140001, 20
+    x = torch.randn(R, V, device="cuda")
+    t = torch.zeros(R, dtype=torch.int32, device="cuda")
+    _, _, tl, tt = mss.token_logprobs(x, t, top=k)
+    for rows in torch.arange(R, device="cuda").split(103):
+        want = x[rows].topk(k, -1)[0]
+        assert torch.equal(x[rows].gather(-1, tt[rows].long()), want)
+        s = tt[rows].sort(-1)[0]
+        assert bool((s[:, 1:] > s[:, :-1]).all())
+    x.zero_()
+    tt = mss.token_logprobs(x, t, top=k)[3]
+    assert torch.equal(tt, torch.arange(k, dtype=torch.int32, device="cuda").expand(R, k))
