@@ -243,6 +243,12 @@ def _logprobs_fwd(logits, tokens, top, logprobs, entropy, top_logprobs, top_toke
             _scratch(floats, logits.device))
 
 
+def _per_token(tokens):
+    import torch
+    first = torch.empty_like(tokens, dtype=torch.float32, memory_format=torch.contiguous_format)
+    return first, torch.empty_like(first)
+
+
 def token_logprobs(logits, tokens, top=0):
     """Log probabilities of given tokens (mss_token_logprobs_fwd), on the current stream: returns (logprobs, entropy),
     or with top > 0 (at most 64) (logprobs, entropy, top_logprobs, top_tokens).
@@ -251,12 +257,11 @@ def token_logprobs(logits, tokens, top=0):
     probability 0).  logprobs, entropy: (...) float32; top_logprobs (..., top) float32 and top_tokens (..., top) int32:
     each row's most probable tokens, best first, equal ones by token; -inf and -1 where there are no more."""
     import torch
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    logprobs, entropy = torch.empty(tokens.shape, **f32), torch.empty(tokens.shape, **f32)
+    logprobs, entropy = _per_token(tokens)
     tops = None, None
     if top:
-        tops = torch.empty((*tokens.shape, top), **f32), torch.empty((*tokens.shape, top), dtype=torch.int32,
-                                                                     device=logits.device)
+        shape = (*tokens.shape, top)
+        tops = tokens.new_empty(shape, dtype=torch.float32), tokens.new_empty(shape, dtype=torch.int32)
     _logprobs_fwd(logits, tokens, int(top), logprobs, entropy, *tops, None)
     return (logprobs, entropy, *tops) if top else (logprobs, entropy)
 
@@ -264,9 +269,8 @@ def token_logprobs(logits, tokens, top=0):
 def token_logprobs_save(logits, tokens):
     """token_logprobs that also returns what its backward needs: (logprobs, entropy, saved), saved (..., 3) float32."""
     import torch
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    logprobs, entropy = torch.empty(tokens.shape, **f32), torch.empty(tokens.shape, **f32)
-    saved = torch.empty((*tokens.shape, 3), **f32)
+    logprobs, entropy = _per_token(tokens)
+    saved = tokens.new_empty((*tokens.shape, 3), dtype=torch.float32)
     _logprobs_fwd(logits, tokens, 0, logprobs, entropy, None, None, saved)
     return logprobs, entropy, saved
 
