@@ -222,7 +222,8 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
     const bool there = SUB == 1 || in_group < a.each;
     const int h = SUB == 1 ? o_head : o_head / ((a.each + SUB - 1) / SUB) * a.each + (there ? in_group : 0);
     const int64_t bh = b * a.H + h;
-    const int64_t len = a.lens ? (a.lens[b] < 0 ? 0 : a.lens[b] < a.L ? a.lens[b] : a.L) : a.L;
+    const int given = a.lens ? __builtin_amdgcn_readfirstlane(a.lens[b]) : 0;
+    const int64_t len = a.lens ? (given < 0 ? 0 : given < a.L ? given : a.L) : a.L;
     const int64_t steps = STATES ? a.part_steps : a.part_steps * a.cuts, from = seg * steps,
                   to = from + steps < a.L ? from + steps : a.L;
     const int64_t stop = to < len ? to : len;                // rows past it are 0
@@ -231,16 +232,23 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
 
     // Rows of a chunk in the order of the walk: row r is token at + r, or, walked backwards, len - 1 - at - r.  A chunk of n
     // rows of a tensor is a buffer that begins at its lowest token; a thread's place in it is an offset.  Rows behind the
-    // end and columns beside the head's lie outside of it, where loads give 0 and stores do nothing.
+    // end and columns beside the head's lie outside of it, where loads give 0 and stores do nothing.  The buffers move from
+    // chunk to chunk by whole rows: addresses made anew for each were a third of a chunk's instructions.
     const bool back = a.back;
-    const auto buffer_of = [&](const void* t, int heads, int head, int dim, int64_t at, int n, int size) MSS_INLINED {
-        const int64_t token = back ? len - at - n : at;
-        const char* p = static_cast<const char*>(t) + ((b * a.L + token) * heads + head) * dim * static_cast<int64_t>(size);
-        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, n * heads * dim * size, 0x00027000);
+    const int todo = stop > from ? static_cast<int>(stop - from) : 0;  // rows of this segment
+    const int64_t token0 = b * a.L + (back ? len - from - (todo < C ? todo : C) : from);
+    const auto start_of = [&](const void* t, int heads, int head, int dim, int size) MSS_INLINED {
+        return static_cast<const char*>(t) + (token0 * heads + head) * dim * static_cast<int64_t>(size);
     };
     constexpr uint32_t kOutside = 0x80000000u;  // no chunk is as large
     const auto offset_of = [&](int row, int row_bytes, int col, bool in, int size) MSS_INLINED {
         return in ? static_cast<uint32_t>((back ? C - 1 - row : row) * row_bytes + col * size) : kOutside;
+    };
+    const auto move = [&](const char*& p, int row_bytes, int n) MSS_INLINED {  // to the next chunk, of n rows
+        p += static_cast<int64_t>((back ? -n : C) * row_bytes);
+    };
+    const auto buffer_at = [](const char* p, int bytes) MSS_INLINED {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, bytes, 0x00027000);
     };
     const int q_row = tid / QU, q_col = tid % QU * 8, v_row = tid / VU, v_col = tid % VU * 8;
     const int q_bytes = a.q.heads * a.Kd * ES, k_bytes = a.k.heads * a.Kd * ES, v_bytes = a.v.heads * a.Vd * ES,
@@ -250,11 +258,17 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
                    v_off = offset_of(v_row, v_bytes, v_col, v_in, ES),
                    o_off = offset_of(r16, o_bytes, v0 + 4 * g, mine, sizeof(O));
 
+    const char* q_at = start_of(a.q.p, a.q.heads, h / (a.H / a.q.heads), a.Kd, ES);
+    const char* k_at = start_of(a.k.p, a.k.heads, h / (a.H / a.k.heads), a.Kd, ES);
+    const char* v_at = start_of(a.v.p, a.v.heads, h / (a.H / a.v.heads), a.Vd, ES);
+    const char* o_at = start_of(a.out, a.outs, o_head, a.Vd, sizeof(O));
+
     Raw<E> rq[STATES ? 1 : NQ], rk[NQ], rv[NV];
-    const auto load = [&](int64_t at, int n) MSS_INLINED {
-        const auto rows = [&](const Rows& t, int dim, int row_bytes, uint32_t off, int step, auto& r) MSS_INLINED {
-            const auto p = buffer_of(t.p, t.heads, h / (a.H / t.heads), dim, at, there ? n : 0, ES);
-            off -= back ? (C - n) * row_bytes : 0;
+    const auto load = [&](int n) MSS_INLINED {
+        const int rows_there = there ? n : 0, missing = back ? C - n : 0;
+        const auto rows = [&](const char* at, int row_bytes, uint32_t off, int step, auto& r) MSS_INLINED {
+            const auto p = buffer_at(at, rows_there * row_bytes);
+            off -= missing * row_bytes;
             const int next = (back ? -step : step) * row_bytes;
 #pragma unroll
             for (int j = 0; j < static_cast<int>(sizeof(r) / sizeof(r[0])); ++j)
@@ -262,27 +276,30 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
                 for (int i = 0; i < kE / E::kPerVec; ++i)
                     r[j].q[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(p, off + j * next + 16 * i, 0, 0));
         };
-        if constexpr (!STATES) rows(a.q, a.Kd, q_bytes, q_off, QR, rq);
-        rows(a.k, a.Kd, k_bytes, k_off, QR, rk);
-        rows(a.v, a.Vd, v_bytes, v_off, VR, rv);
+        if constexpr (!STATES) rows(q_at, q_bytes, q_off, QR, rq);
+        rows(k_at, k_bytes, k_off, QR, rk);
+        rows(v_at, v_bytes, v_off, VR, rv);
     };
-    const auto put = [&](Raw<E> r, uint16_t* p, int plane, bool swap) MSS_INLINED {
+    const auto put = [&](const Raw<E>& r, int plane, auto write) MSS_INLINED {
         if constexpr (NP == 1) {
-            const uint4 q = r.q[0];
-            *reinterpret_cast<uint4*>(p) = swap ? make_uint4(q.z, q.w, q.x, q.y) : q;
+            write(r.q[0], 0);
         } else {
-            if (swap) {
-                const uint4 q = r.q[0];
-                r.q[0] = r.q[1];
-                r.q[1] = q;
-            }
             float x[kE];
             r.unpack(x);
             s16x8 part[NP];
             cut<NP>(x, part);
 #pragma unroll
-            for (int n = 0; n < NP; ++n) *reinterpret_cast<s16x8*>(p + n * plane) = part[n];
+            for (int n = 0; n < NP; ++n) write(__builtin_bit_cast(uint4, part[n]), n * plane);
         }
+    };
+    const auto put8 = [&](const Raw<E>& r, uint16_t* p, int plane) MSS_INLINED {
+        put(r, plane, [&](uint4 q, int to) MSS_INLINED { *reinterpret_cast<uint4*>(p + to) = q; });
+    };
+    const auto put4 = [&](const Raw<E>& r, uint16_t* lo, uint16_t* hi, int plane) MSS_INLINED {
+        put(r, plane, [&](uint4 q, int to) MSS_INLINED {
+            *reinterpret_cast<uint2*>(lo + to) = make_uint2(q.x, q.y);
+            *reinterpret_cast<uint2*>(hi + to) = make_uint2(q.z, q.w);
+        });
     };
     const auto key_at = [](int row, int col) MSS_INLINED { return col ^ (row & 8) >> 1 ^ (row & 4) << 2; };
     const auto value_at = [](int row, int col) MSS_INLINED { return col ^ (row & 8) * (VT / 32); };
@@ -291,12 +308,12 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
                 const int row = q_row + j * QR;
-                if constexpr (!STATES) put(rq[j], &qs[0][row][q_col], C * QS, false);
-                put(rk[j], &ks[0][row][key_at(row, q_col) & ~7], C * KS, row & 8);  // (halves of 16 bytes as key_at has them)
+                if constexpr (!STATES) put8(rq[j], &qs[0][row][q_col], C * QS);
+                put4(rk[j], &ks[0][row][key_at(row, q_col)], &ks[0][row][key_at(row, q_col + 4)], C * KS);
             }
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) put(rv[j], &vs[0][v_row + j * VR][value_at(v_row + j * VR, v_col)], C * VS, false);
+        for (int j = 0; j < NV; ++j) put8(rv[j], &vs[0][v_row + j * VR][value_at(v_row + j * VR, v_col)], C * VS);
     };
     // eight values of a column, rows 32 m + 8 g ...
     const auto read_values = [&](int m, s16x8* f) MSS_INLINED {
@@ -316,15 +333,17 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
     float small[8];  // l^0 .. l^7, in scalar registers: the powers of a lane's rows are products of one of its own and these
 #pragma unroll
     for (int e = 0; e < 8; ++e) small[e] = uniform(power(e));
-    float near[4];
+    // The scores of a chunk are three tiles, one to each of the first three waves: (ta, tb) = (0, 0), (0, 1), (1, 1).
+    static_assert(MT == 2 && NW >= 3, "a wave has at most one tile of scores");
+    const int ta = wave >> 1, tb_of_wave = (wave + 1) >> 1;
+    float decay[4];  // of this wave's tile
 #pragma unroll
-    for (int i = 0; i < 4; ++i) near[i] = power(r16 >= 4 * g + i ? r16 - 4 * g - i : 0) * (a.s_add * a.s_out);
-    const float off = power(13 + r16 - 4 * g) * (a.s_add * a.s_out), since = power(r16) * a.s_out,
-                tail = power(24 - 8 * g) * a.s_add;
+    for (int i = 0; i < 4; ++i) {
+        const int steps = 16 * (tb_of_wave - ta) + r16 - 4 * g - i;
+        decay[i] = power(steps > 0 ? steps : 0) * (a.s_add * a.s_out);
+    }
+    const float since = power(r16) * a.s_out, tail = power(24 - 8 * g) * a.s_add, step16 = uniform(power(16));
     const float tail32 = uniform(power(32)), less = uniform(expm1f(-rate * C));
-    // steps that the state decays by in a chunk of n rows; walked backwards, it enters the first row undecayed
-    const auto decays = [&](int64_t at, int n) MSS_INLINED { return back && at == 0 ? n - 1 : n; };
-
     // The state: tile j holds rows 32 (j / 2) + 8 g + 4 (j % 2) + i of a column, so that two tiles are eight rows in turn.
     f32x4 st[KT];
     const int64_t per = static_cast<int64_t>(a.Kd) * a.Vd;
@@ -350,11 +369,10 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         const int row = 8 * g + (r16 >> 2) + 4 * (i % 2);
         turned[i / 2][i % 2] = &ks[0][row][key_at(row, 8 * (r16 & 3) + 4 * (i / 2))];
     }
-    const auto rows_at = [&](int64_t at) MSS_INLINED {  // rows of a chunk
-        const int64_t n = stop - at;
-        return static_cast<int>(n < 0 ? 0 : n < C ? n : C);
+    const auto rows_at = [&](int at) MSS_INLINED {  // of a chunk (the compiler takes the vector unit's median for it)
+        return __builtin_amdgcn_readfirstlane(todo - at < 0 ? 0 : todo - at < C ? todo - at : C);
     };
-    load(from, rows_at(from));
+    load(rows_at(0));
     if constexpr (!STATES) {
         // the state before the segment: what the join kernel made of it, or the first one and what the parts before add
         const bool joined = a.nparts > kFold && seg > 0;
@@ -368,83 +386,88 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         for (int e = tid; e < NS * C * PS / 8; e += T) reinterpret_cast<uint4*>(&ps[0][0][0])[e] = make_uint4(0, 0, 0, 0);
     }
 
-    const auto write = [&](int64_t at, int n, const f32x4* acc) MSS_INLINED {
-                    const auto o = buffer_of(a.out, a.outs, o_head, a.Vd, at, n, sizeof(O));
-                    const uint32_t first = o_off - (back ? (C - n) * o_bytes : 0);
+    const auto write = [&](int n, const f32x4* acc) MSS_INLINED {
+        const auto o = buffer_at(o_at, n * o_bytes);
+        const uint32_t first = o_off - (back ? C - n : 0) * o_bytes;
 #pragma unroll
-                    for (int tb = 0; tb < MT; ++tb) {
-                        const uint32_t off = first + (back ? -16 : 16) * tb * o_bytes;
-                        const f32x4 x = acc[tb];
-                        if constexpr (sizeof(O) == 2)
-                            __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, o, off, 0, 0);
-                        else
-                            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), o, off, 0, 0);
-                    }
+        for (int tb = 0; tb < MT; ++tb) {
+            const uint32_t off = first + (back ? -16 : 16) * tb * o_bytes;
+            const f32x4 x = acc[tb];
+            if constexpr (sizeof(O) == 2)
+                __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])}, o, off, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), o, off, 0, 0);
+        }
     };
-    for (int64_t at = from; at < stop; at += C) {
-        const int n = rows_at(at);
+    // what the state's part of an output decays by; walked backwards, the state enters the sequence's first row undecayed
+    const bool keep = !STATES && a.last && seg == a.nseg - 1;
+    int early = back && from == 0 ? 1 : 0;
+    float faded = since * power(1 - early);
+    for (int at = 0; at < todo; at += C) {
+        const int n = rows_at(at), ahead = rows_at(at + C);
         store();
+        move(q_at, q_bytes, ahead);
+        move(k_at, k_bytes, ahead);
+        move(v_at, v_bytes, ahead);
         __syncthreads();
-        load(at + C, rows_at(at + C));
+        load(ahead);
         s16x8 vf[M2][NP];
         f32x4 acc[MT];
         if constexpr (!STATES) {
-            // scores: the tiles (ta <= tb) in turn to the waves
-            constexpr int tiles = MT * (MT + 1) / 2;
-            for (int tile = wave; tile < tiles; tile += NW) {
-                int tb = 0, ta = tile;
-                while (ta > tb) ta -= ++tb;
-                s16x8 qf[KJ][NP], kf[KJ][NP];
-#pragma unroll
-                for (int j = 0; j < KJ; ++j)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        qf[j][p] = *reinterpret_cast<const s16x8*>(&qs[p][16 * tb + r16][32 * j + 8 * g]);
-                        const uint16_t* row = ks[p][16 * ta + r16] + 32 * j;  // (key_at moves columns within 32)
-                        kf[j][p] = join8(*reinterpret_cast<const s16x4*>(row + key_at(r16, 8 * g)),
-                                         *reinterpret_cast<const s16x4*>(row + key_at(r16, 8 * g + 4)));
-                    }
-                issue_reads();
+            if (wave < 3) {  // scores
+                constexpr int G = NP == 1 && NW == 4 ? 2 : KJ;  // as many at once as registers hold
                 f32x4 p4 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < KJ; ++j) p4 = mma_parts<NP, NP>(kf[j], qf[j], p4);
-                if (ta == tb) {
+                for (int j0 = 0; j0 < KJ; j0 += G) {
+                    s16x8 qf[G][NP], kf[G][NP];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p4[i] = r16 >= 4 * g + i ? p4[i] * near[i] : 0.0f;
-                    }
-                } else {
-                    const float f = off * power(16 * (tb - ta - 1));
+                    for (int j = 0; j < G; ++j)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p4[i] *= f * small[3 - i];
+                        for (int p = 0; p < NP; ++p) {
+                            qf[j][p] = *reinterpret_cast<const s16x8*>(&qs[p][16 * tb_of_wave + r16][32 * (j0 + j) + 8 * g]);
+                            const uint16_t* row = ks[p][16 * ta + r16] + 32 * (j0 + j);  // (key_at moves columns within 32)
+                            kf[j][p] = join8(*reinterpret_cast<const s16x4*>(row + key_at(r16, 8 * g)),
+                                             *reinterpret_cast<const s16x4*>(row + key_at(r16, 8 * g + 4)));
+                        }
+                    issue_reads();
+#pragma unroll
+                    for (int j = 0; j < G; ++j) p4 = mma_parts<NP, NP>(kf[j], qf[j], p4);
                 }
                 uint32_t w[NS][2];
-                float x[4] = {p4[0], p4[1], p4[2], p4[3]};
+                float x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[i] = wave == 1 || r16 >= 4 * g + i ? p4[i] * decay[i] : 0.0f;
                 cut_words<NS, 2>(x, w);
 #pragma unroll
                 for (int p = 0; p < NS; ++p)
-                    *reinterpret_cast<uint2*>(&ps[p][16 * tb + r16][16 * ta + 4 * g]) = make_uint2(w[p][0], w[p][1]);
+                    *reinterpret_cast<uint2*>(&ps[p][16 * tb_of_wave + r16][16 * ta + 4 * g]) = make_uint2(w[p][0], w[p][1]);
             }
             // what the state before the chunk gives: rows of a tile are columns v, lanes are steps t
 #pragma unroll
             for (int tb = 0; tb < MT; ++tb) acc[tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = 0; j < KJ; ++j) {
-                s16x8 qf[MT][NP], sf[NS];
+            constexpr int B = SUB == 1 && (NP > 1 || NW == 8 || KD == 64) ? 2 : 1;  // 2: the next step's are read ahead
+            s16x8 qf[B][MT][NP];
+            const auto read_queries = [&](int j) MSS_INLINED {
 #pragma unroll
                 for (int tb = 0; tb < MT; ++tb)
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
-                        qf[tb][p] = *reinterpret_cast<const s16x8*>(&qs[p][16 * tb + r16][32 * j + 8 * g]);
+                        qf[j % B][tb][p] = *reinterpret_cast<const s16x8*>(&qs[p][16 * tb + r16][32 * j + 8 * g]);
                 issue_reads();
+            };
+            if (B == 2) read_queries(0);
+#pragma unroll
+            for (int j = 0; j < KJ; ++j) {
+                if (B == 1 || j + 1 < KJ) read_queries(j + B - 1);
+                s16x8 sf[NS];
                 float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[i] = st[2 * j][i], x[4 + i] = st[2 * j + 1][i];
                 cut<NS>(x, sf);
-                mma_each<MT, NS, NP>([&](int) MSS_INLINED { return sf; }, [&](int tb) MSS_INLINED { return qf[tb]; }, acc);
+                mma_each<MT, NS, NP>([&](int) MSS_INLINED { return sf; }, [&](int tb) MSS_INLINED { return qf[j % B][tb]; }, acc);
             }
 #pragma unroll
-            for (int tb = 0; tb < MT; ++tb) acc[tb] *= since * power(16 * tb + (back && at == 0 ? 0 : 1));
+            for (int tb = 0; tb < MT; ++tb) acc[tb] *= tb ? faded * step16 : faded;
             __syncthreads();
 #pragma unroll
             for (int m = 0; m < M2; ++m) {
@@ -463,7 +486,7 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
                             if (i + j < NS) acc[tb] = mma(vf[m][i], pf[tb], acc[tb]);
                 }
             }
-            if (SUB == 1) write(at, n, acc);
+            if (SUB == 1) write(n, acc);
             else if (sub > 0) {
 #pragma unroll
                 for (int tb = 0; tb < MT; ++tb) others[sub - 1][tb][tid] = acc[tb];
@@ -473,9 +496,8 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
             for (int m = 0; m < M2; ++m) read_values(m, vf[m]);
         }
         // the state after the chunk, if it is read
-        if (STATES || at + C < stop || (a.last && seg == a.nseg - 1)) {
-            const int d = decays(at, n);
-            const float gone = d == C ? less : expm1f(-rate * static_cast<float>(d));
+        if (STATES || ahead || keep) {
+            const float gone = n - early == C ? less : expm1f(-rate * static_cast<float>(n - early));
 #pragma unroll
             for (int j = 0; j < KT; ++j)
 #pragma unroll
@@ -501,7 +523,7 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
                 }
                 s16x8 wf[3];
                 cut<3>(x, wf);
-                constexpr int G = 4;  // tiles at once
+                constexpr int G = NP == 1 && SUB == 4 ? 2 : 4;  // tiles at once
 #pragma unroll
                 for (int j0 = 0; j0 < KT; j0 += G) {
                     s16x8 kt[G][NP];
@@ -523,7 +545,12 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
             for (int x = 0; x < SUB - 1; ++x)
 #pragma unroll
                 for (int tb = 0; tb < MT; ++tb) acc[tb] += others[x][tb][tid];
-            write(at, n, acc);
+            write(n, acc);
+        }
+        move(o_at, o_bytes, ahead);
+        if (early) {
+            early = 0;
+            faded = since * power(1);
         }
     }
     if (!mine) return;
@@ -536,7 +563,7 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
             if (sizeof(O) == 2) *reinterpret_cast<uint2*>(p) = make_uint2(0, 0);
             else *reinterpret_cast<f32x4*>(p) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        if (a.last && seg == a.nseg - 1) {
+        if (keep) {
             // walked backwards, the state is that of the first step: the one before it is a step further
             const float f = back && len > 0 ? power(1) : 1.0f;
             float* p = a.last + bh * per;
