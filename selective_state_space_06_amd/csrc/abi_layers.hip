@@ -35,7 +35,8 @@ int check_sizes(int64_t Bt, int64_t L, int64_t H, int64_t Hq, int64_t Hk, int64_
     if (H > 32768) return MSS_ERR_UNSUPPORTED;  // a chunk's offsets are 32 bits
     if (K % 16 || V % 16 || K > mss::kAttnMostDim || V > mss::kAttnMostDim) return MSS_ERR_UNSUPPORTED;
     int64_t n = 0;
-    if (__builtin_mul_overflow(Bt, H, &n) || n > (int64_t{1} << 28)) return MSS_ERR_UNSUPPORTED;  // blocks
+    if (L > INT32_MAX) return MSS_ERR_UNSUPPORTED;
+    if (__builtin_mul_overflow(Bt, H, &n) || n > (int64_t{1} << 20)) return MSS_ERR_UNSUPPORTED;  // 2^32 threads a launch
     if (__builtin_mul_overflow(n, L, &n) || n > (int64_t{1} << 40)) return MSS_ERR_UNSUPPORTED;
     return MSS_OK;
 }
@@ -143,11 +144,12 @@ int mss_linear_attention_scratch(int64_t batch, int64_t L, int64_t heads, int64_
     const int st = check_sizes(batch, L, heads, q_heads, k_heads, v_heads, key_dim, value_dim);
     if (st != MSS_OK) return st;
     const auto n = [](int64_t v) { return static_cast<int>(v); };
-    *fwd = mss::attn_fwd_scratch(batch, L, n(heads), n(key_dim), n(value_dim));
-    *bwd = 0;
-    for (const bool bf16 : {false, true})  // what either type needs
+    *fwd = *bwd = 0;
+    for (const bool bf16 : {false, true}) {  // what either type needs
+        *fwd = std::max(*fwd, mss::attn_fwd_scratch(batch, L, n(heads), n(key_dim), n(value_dim), bf16));
         *bwd = std::max(*bwd, mss::attn_bwd_scratch(batch, L, n(heads), n(q_heads), n(k_heads), n(v_heads), n(key_dim),
                                                     n(value_dim), bf16));
+    }
     return MSS_OK;
 }
 
@@ -177,7 +179,8 @@ int mss_linear_attention_fwd(const mss_tensor_t* q, const mss_tensor_t* k, const
             return MSS_ERR_LAYOUT;
         if (st != MSS_OK) return st;
         const int h = static_cast<int>(H);
-        st = check_scratch(scratch, mss::attn_fwd_scratch(Bt, L, h, static_cast<int>(K), static_cast<int>(V)));
+        st = check_scratch(scratch, mss::attn_fwd_scratch(Bt, L, h, static_cast<int>(K), static_cast<int>(V),
+                                                           q->dtype == MSS_BF16));
         if (st != MSS_OK) return st;
         if (!apart({q, k, v, rate, initial_state, seq_lens}, {out, last_state, scratch})) return MSS_ERR_ALIAS;
         mss::AttnLaunch a;

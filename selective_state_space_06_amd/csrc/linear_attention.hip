@@ -573,28 +573,36 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
 }
 
 // The states that enter the segments but the first, from what the parts add, in place (in the last part of the segment
-// before): a block per (batch, head) and 256 elements.
+// before): a block per (batch, head) and 256 elements.  The parts' decays are made once for the block, not by every thread.
 __global__ __launch_bounds__(256) void attention_join_kernel(Walks all, int blocks) {
+    __shared__ float gone[256];
     const AArgs& a = all.w[blockIdx.x / all.each];
     const int64_t block = blockIdx.x % all.each, bh = block / blocks, b = bh / a.H;
     const int per = a.Kd * a.Vd, x = static_cast<int>(block % blocks) * 256 + threadIdx.x;
-    if (x >= per) return;
     const int64_t len = a.lens ? (a.lens[b] < 0 ? 0 : a.lens[b] < a.L ? a.lens[b] : a.L) : a.L;
     const float rate = fminf(fmaxf(a.rate[bh % a.H], 0.0f), kMostRate);
     float s = 0.0f;
-    if (a.init) s = a.init[bh * per + (a.turned ? x % a.Vd * a.Kd + x / a.Vd : x)];
-    float* o = a.parts + bh * a.nparts * per + x;
+    if (a.init && x < per) s = a.init[bh * per + (a.turned ? x % a.Vd * a.Kd + x / a.Vd : x)];
+    float* o = a.parts + bh * a.nparts * per + (x < per ? x : 0);
     constexpr int G = 16;  // on their way at once
+    int left = a.cuts;     // parts of this segment: the last gives the next one's state, the others what no one reads
     for (int i0 = 0; i0 < a.nparts; i0 += G) {
+        if (i0 % 256 == 0) {
+            __syncthreads();
+            if (i0 + static_cast<int>(threadIdx.x) < a.nparts) gone[threadIdx.x] = part_decay(a, rate, len, i0 + threadIdx.x);
+            __syncthreads();
+        }
         float adds[G];
 #pragma unroll
         for (int i = 0; i < G; ++i) adds[i] = o[static_cast<int64_t>(i0 + i < a.nparts ? i0 + i : i0) * per];
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             if (i0 + i >= a.nparts) break;
-            s = fmaf(s, part_decay(a, rate, len, i0 + i), s) + adds[i];
-            // (parts before the last of a segment hold what no one reads; the segment's last gives the next one's state)
-            if ((i0 + i + 1) % a.cuts == 0) o[static_cast<int64_t>(i0 + i) * per] = s;
+            s = fmaf(s, gone[(i0 + i) % 256], s) + adds[i];
+            if (--left == 0) {
+                left = a.cuts;
+                if (x < per) o[static_cast<int64_t>(i0 + i) * per] = s;
+            }
         }
     }
 }
@@ -659,35 +667,37 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
     }
 }
 
-// How a sequence is cut.  A block walks a segment in about the same time for every 64 steps (4 us with 128 keys), and a CU
+// How a sequence is cut.  A block walks a segment in about the same time for every 64 steps (3.5 us with 128 keys), and a CU
 // with more than one block takes longer by what they share: measured for c blocks of eight waves 0.9 c, for four waves
-// 0.1 + 0.7 c, for 16 waves, which do not fit twice, 1.3 c.  The start of a segment is worth one such time.  More segments
-// fill the CUs better but need the states between them: a pass over keys and values at 0.6 (eight waves) or 0.4 (four) of
-// the walk, and a launch.  That pass, whose blocks wait for nothing, is cut further, into parts of 128 steps or more, up
-// to two blocks for every CU.
-// Times by the number of segments, the one that is taken in brackets: 4 x 2048 x 32 heads of 128 x 128 bf16, 1 to 4: 142,
-// [118], 119, 129 us; 3 x 1531 x 12 heads of 64 x 96 f32, 4, 6, 8, 16: 68, [60], 79, 65; 1 x 2048 x 32 heads of 128 x 128
-// bf16 with shared keys and values, 4, 6, 8, 16: 73, 64, [59], 61.
+// 0.1 + 0.7 c, for 16 waves 1.3; blocks that find no room (16 waves a CU, eight in fp32) come after.  The start of a segment
+// is worth one such time.  More segments fill the CUs better but need the states between them: a pass over keys and values at
+// 0.6 (eight waves) or 0.3 (four) of the walk, and a launch.  That pass, whose blocks wait for nothing, is cut further, into
+// parts of 128 steps or more, up to a block for every CU.
+// Times by the number of segments, the one that is taken in brackets: 4 x 2048 x 32 heads of 128 x 128 bf16, 1 to 4: 121,
+// [104], 113, 120 us; 4 x 2048 x 80 of 128 x 64 bf16: 127, 125, [117], 128; 3 x 1531 x 12 of 64 x 96 f32, 4, 6, 8, 16: 55,
+// [51], 66, 53; 1 x 2048 x 32 of 128 x 128 bf16, keys and values of 8 heads, 4, 6, 8, 16: 65, 60, [55], 56.
 struct Plan {
     int nseg, nparts, cuts;
     int64_t part_steps;
 };
 // blocks: of each segment; heads: whose states are wanted; waves: of a block, of one of those that make states
-Plan plan_segments(int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
-    const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64);
+Plan plan_segments(bool bf16, int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
+    const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64), most = std::max(1, (bf16 ? 16 : 8) / waves);
+    const auto time_of = [&](int64_t c) {
+        return waves == 16 ? 13 * c : std::max<int64_t>(c > 0 ? 10 : 0, waves == 8 ? 9 * c : 1 + 7 * c);
+    };
     int64_t best = 0, segment = steps64;
     for (int64_t n = 1; n <= std::min<int64_t>(64, steps64 / 2 + 1); ++n) {
         const int64_t each = (steps64 + n - 1) / n, segs = (steps64 + each - 1) / each;  // of 64 steps, and how many there are
         const int64_t c = (blocks * segs + 255) / 256;
-        const int64_t per = waves == 16 ? 13 * c : std::max<int64_t>(10, waves == 8 ? 9 * c : 1 + 7 * c);
-        int64_t cost = per * (each + 1);
-        if (segs > 1) cost += (state_waves == 8 ? 6 : 4) * heads * (segs - 1) * each / 256 + 15;
+        int64_t cost = (c / most * time_of(most) + (c % most ? time_of(c % most) : 0)) * (each + 1);
+        if (segs > 1) cost += (state_waves == 8 ? 6 : 3) * heads * (segs - 1) * each / 256 + 15;
         if (n == 1 || cost < best) best = cost, segment = each;
     }
     Plan p;
     p.nseg = static_cast<int>((steps64 + segment - 1) / segment);
     p.cuts = 1;
-    while (p.nseg > 1 && segment % (2 * p.cuts) == 0 && segment / (2 * p.cuts) >= 2 && heads * (p.nseg - 1) * p.cuts < 512)
+    while (p.nseg > 1 && segment % (2 * p.cuts) == 0 && segment / (2 * p.cuts) >= 2 && heads * (p.nseg - 1) * p.cuts < 256)
         p.cuts *= 2;
     p.part_steps = segment * 64 / p.cuts;
     p.nparts = (p.nseg - 1) * p.cuts;
@@ -700,7 +710,7 @@ constexpr int heads_at_once(bool bf16, int KD, int NW) { return bf16 ? 16 / NW :
 
 Plan plan_walks(bool bf16, int64_t Bt, int64_t L, int H, int outs, int each, int Kd, int Vd, int count) {
     const int waves = columns(Vd) / 16;
-    return plan_segments(Bt * outs * count, Bt * H * count,
+    return plan_segments(bf16, Bt * outs * count, Bt * H * count,
                          each > 1 ? waves * heads_at_once(bf16, Kd <= 64 ? 64 : 128, waves) : waves, waves, L);
 }
 
@@ -822,8 +832,8 @@ void backward(const AttnLaunch& l, hipStream_t s) {
 
 }  // namespace
 
-int64_t attn_fwd_scratch(int64_t Bt, int64_t L, int H, int K, int V) {
-    return Bt * H * plan_walks(true, Bt, L, H, H, 1, K, V, 1).nparts * K * V;
+int64_t attn_fwd_scratch(int64_t Bt, int64_t L, int H, int K, int V, bool bf16) {
+    return Bt * H * plan_walks(bf16, Bt, L, H, H, 1, K, V, 1).nparts * K * V;
 }
 
 int64_t attn_bwd_scratch(int64_t Bt, int64_t L, int H, int Hq, int Hk, int Hv, int K, int V, bool bf16) {

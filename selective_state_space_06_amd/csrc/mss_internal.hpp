@@ -331,7 +331,7 @@ struct AttnUpdateLaunch {
     float scale;
     bool bf16;
 };
-int64_t attn_fwd_scratch(int64_t Bt, int64_t L, int H, int K, int V);
+int64_t attn_fwd_scratch(int64_t Bt, int64_t L, int H, int K, int V, bool bf16);
 int64_t attn_bwd_scratch(int64_t Bt, int64_t L, int H, int Hq, int Hk, int Hv, int K, int V, bool bf16);
 hipError_t launch_attn_fwd(const AttnLaunch& a, hipStream_t stream);
 hipError_t launch_attn_bwd(const AttnLaunch& a, hipStream_t stream);

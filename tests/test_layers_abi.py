@@ -270,6 +270,9 @@ def test_scratch_queries():
                           (mss.linear_attention_scratch, (1, 5, 6, 4, 6, 6, 16, 16), SHAPE),
                           (mss.linear_attention_scratch, (1, 5, 6, 6, 6, 6, 20, 16), UNSUPPORTED),
                           (mss.linear_attention_scratch, (1 << 40, 5, 6, 6, 6, 6, 16, 16), UNSUPPORTED),
+                          (mss.linear_attention_scratch, (1, 1 << 31, 1, 1, 1, 1, 16, 16), UNSUPPORTED),
+                          (mss.linear_attention_scratch, (1, 5, 32769, 1, 1, 1, 16, 16), UNSUPPORTED),
+                          (mss.linear_attention_scratch, (1 << 15, 5, 64, 1, 1, 1, 16, 16), UNSUPPORTED),
                           (mss.linear_attention_scratch, (1, -1, 6, 6, 6, 6, 16, 16), SHAPE),
                           (mss.token_logprobs_scratch, (4, 0, 1), SHAPE), (mss.token_logprobs_scratch, (4, 9, 65), UNSUPPORTED),
                           (mss.token_logprobs_scratch, (4, 1 << 31, 0), UNSUPPORTED)):
