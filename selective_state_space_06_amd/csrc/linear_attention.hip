@@ -678,11 +678,12 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
 // [51], 66, 53; 1 x 2048 x 32 of 128 x 128 bf16, keys and values of 8 heads, 4, 6, 8, 16: 65, 60, [55], 56.
 struct Plan {
     int nseg, nparts, cuts;
-    int64_t part_steps;
+    int64_t part_steps, cost;
 };
+int blocks_a_cu(bool bf16, int waves) { return std::max(1, (bf16 ? 16 : 8) / waves); }
 // blocks: of each segment; heads: whose states are wanted; waves: of a block, of one of those that make states
 Plan plan_segments(bool bf16, int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
-    const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64), most = std::max(1, (bf16 ? 16 : 8) / waves);
+    const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64), most = blocks_a_cu(bf16, waves);
     const auto time_of = [&](int64_t c) {
         return waves == 16 ? 13 * c : std::max<int64_t>(c > 0 ? 10 : 0, waves == 8 ? 9 * c : 1 + 7 * c);
     };
@@ -695,6 +696,7 @@ Plan plan_segments(bool bf16, int64_t blocks, int64_t heads, int waves, int stat
         if (n == 1 || cost < best) best = cost, segment = each;
     }
     Plan p;
+    p.cost = best;
     p.nseg = static_cast<int>((steps64 + segment - 1) / segment);
     p.cuts = 1;
     while (p.nseg > 1 && segment % (2 * p.cuts) == 0 && segment / (2 * p.cuts) >= 2 && heads * (p.nseg - 1) * p.cuts < 256)
@@ -708,10 +710,37 @@ int columns(int Vd) { return Vd > 64 ? 128 : 64; }
 // Heads of a group that a block does: 16 waves of bf16's kernels find room on a CU, eight of fp32's smallest.
 constexpr int heads_at_once(bool bf16, int KD, int NW) { return bf16 ? 16 / NW : KD == 64 && NW == 4 ? 2 : 1; }
 
-Plan plan_walks(bool bf16, int64_t Bt, int64_t L, int H, int outs, int each, int Kd, int Vd, int count) {
-    const int waves = columns(Vd) / 16;
-    return plan_segments(bf16, Bt * outs * count, Bt * H * count,
-                         each > 1 ? waves * heads_at_once(bf16, Kd <= 64 ? 64 : 128, waves) : waves, waves, L);
+// Sizes of the walks of a launch.
+struct Sizes {
+    bool bf16;
+    int64_t Bt, L;
+    int H, outs, each, Kd, Vd, count;
+    int waves() const {
+        const int w = columns(Vd) / 16;
+        return each > 1 ? w * heads_at_once(bf16, Kd <= 64 ? 64 : 128, w) : w;
+    }
+    Sizes of(int64_t batches) const {
+        Sizes s = *this;
+        s.Bt = batches;
+        return s;
+    }
+};
+Plan plan_walks(const Sizes& z) {
+    return plan_segments(z.bf16, z.Bt * z.outs * z.count, z.Bt * z.H * z.count, z.waves(), columns(z.Vd) / 16, z.L);
+}
+// Batches of a first launch: all, or as many as fill the CUs in whole rounds, when the others, cut finer, are done sooner in
+// one of their own than as the rest of a round (320 blocks of 16 waves: 182 + 64 us and 29 for the states, 327 in one launch).
+int64_t first_batches(const Sizes& z) {
+    const int64_t blocks = z.outs * z.count, room = 256 * blocks_a_cu(z.bf16, z.waves());
+    const int64_t first = z.Bt * blocks / room * room / blocks;
+    if (first < 1 || first == z.Bt) return z.Bt;
+    return plan_walks(z.of(first)).cost + plan_walks(z.of(z.Bt - first)).cost + 15 < plan_walks(z).cost ? first : z.Bt;
+}
+int64_t state_floats(const Sizes& z) {
+    const int64_t first = first_batches(z), rest = z.Bt - first;
+    int64_t n = first * plan_walks(z.of(first)).nparts;
+    if (rest) n = std::max(n, rest * plan_walks(z.of(rest)).nparts);
+    return z.count * n * z.H * z.Kd * z.Vd;
 }
 
 template <class E, class OUT, int KD, int NW>
@@ -737,24 +766,44 @@ void walk_waves(Walks& w, int count, hipStream_t s) {
     }
     attention_kernel<E, OUT, KD, NW, 1, false><<<grid(blocks), block, 0, s>>>(w);
 }
-// Walks of the same sizes and type of outputs, side by side; their states in scratch.
+// Walks of the same sizes and type of outputs, side by side, of some batches; their states in scratch.
 template <class E, class OUT>
-void walk(Walks& w, int count, float* scratch, hipStream_t s) {
-    const Plan p = plan_walks(Form<E>::NP == 1, w.w[0].Bt, w.w[0].L, w.w[0].H, w.w[0].outs, w.w[0].each, w.w[0].Kd,
-                              w.w[0].Vd, count);
-    for (int i = 0; i < count; ++i) {
+void walk_batches(Walks w, const Sizes& z, int64_t from, float* scratch, hipStream_t s) {
+    const Plan p = plan_walks(z);
+    for (int i = 0; i < z.count; ++i) {
         AArgs& a = w.w[i];
+        const auto rows = [&](const void* t, int64_t row, size_t size) {
+            return static_cast<const char*>(t) + from * z.L * row * static_cast<int64_t>(size);
+        };
+        constexpr size_t ES = sizeof(typename E::storage);
+        const int64_t states = from * z.H * z.Kd * z.Vd;
+        a.q.p = rows(a.q.p, a.q.heads * z.Kd, ES);
+        a.k.p = rows(a.k.p, a.k.heads * z.Kd, ES);
+        a.v.p = rows(a.v.p, a.v.heads * z.Vd, ES);
+        a.out = const_cast<char*>(rows(a.out, z.outs * z.Vd, sizeof(typename OUT::storage)));
+        if (a.lens) a.lens += from;
+        if (a.init) a.init += states;
+        if (a.last) a.last += states;
+        a.Bt = z.Bt;
         a.nseg = p.nseg; a.nparts = p.nparts; a.cuts = p.cuts; a.part_steps = p.part_steps;
-        a.parts = scratch + i * a.Bt * a.H * p.nparts * a.Kd * a.Vd;
+        a.parts = scratch + i * z.Bt * z.H * p.nparts * z.Kd * z.Vd;
     }
-    const bool wide = columns(w.w[0].Vd) == 128;
-    if (w.w[0].Kd <= 64) {
-        if (wide) walk_waves<E, OUT, 64, 8>(w, count, s);
-        else walk_waves<E, OUT, 64, 4>(w, count, s);
+    const bool wide = columns(z.Vd) == 128;
+    if (z.Kd <= 64) {
+        if (wide) walk_waves<E, OUT, 64, 8>(w, z.count, s);
+        else walk_waves<E, OUT, 64, 4>(w, z.count, s);
     } else {
-        if (wide) walk_waves<E, OUT, 128, 8>(w, count, s);
-        else walk_waves<E, OUT, 128, 4>(w, count, s);
+        if (wide) walk_waves<E, OUT, 128, 8>(w, z.count, s);
+        else walk_waves<E, OUT, 128, 4>(w, z.count, s);
     }
+}
+template <class E, class OUT>
+void walk(const Walks& w, int count, float* scratch, hipStream_t s) {
+    const AArgs& a = w.w[0];
+    const Sizes z{Form<E>::NP == 1, a.Bt, a.L, a.H, a.outs, a.each, a.Kd, a.Vd, count};
+    const int64_t first = first_batches(z);
+    walk_batches<E, OUT>(w, z.of(first), 0, scratch, s);
+    if (first < a.Bt) walk_batches<E, OUT>(w, z.of(a.Bt - first), first, scratch, s);
 }
 
 // The backward's walks: of what sizes, from and to where.  Those of equal sizes whose outputs are alike go in one launch.
@@ -792,8 +841,7 @@ Roles roles_of(const AttnLaunch& l) {
 }
 // Floats of scratch of a launch's states, and of a walk's sums before they are added up.
 int64_t states_of(const AttnLaunch& l, const Role& r, int count) {
-    return count * l.Bt * l.H * l.K * l.V *
-           plan_walks(l.bf16, l.Bt, l.L, l.H, r.outs, r.each, r.Kd, r.Vd, count).nparts;
+    return state_floats({l.bf16, l.Bt, l.L, l.H, r.outs, r.each, r.Kd, r.Vd, count});
 }
 int64_t sums_of(const AttnLaunch& l, const Role& r) { return r.sums > 1 ? l.Bt * l.L * r.outs * r.Vd : 0; }
 
@@ -833,7 +881,7 @@ void backward(const AttnLaunch& l, hipStream_t s) {
 }  // namespace
 
 int64_t attn_fwd_scratch(int64_t Bt, int64_t L, int H, int K, int V, bool bf16) {
-    return Bt * H * plan_walks(bf16, Bt, L, H, H, 1, K, V, 1).nparts * K * V;
+    return state_floats({bf16, Bt, L, H, H, 1, K, V, 1});
 }
 
 int64_t attn_bwd_scratch(int64_t Bt, int64_t L, int H, int Hq, int Hk, int Hv, int K, int V, bool bf16) {

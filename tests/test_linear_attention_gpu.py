@@ -123,6 +123,14 @@ def test_few_heads_cut_in_segments(mss, B, L, H, K, V, lens, dtype):
     check(mss, inputs(B, L, H, K, V, dtype, lens=lens, state=True, seed=L))
 
 
+@pytest.mark.parametrize("B,L,H,K,V,heads,dtype,gradients", [
+    (11, 500, 40, 16, 16, (4, 4, 40), "bf16", True), (7, 500, 40, 16, 16, (4, 4, 40), "f32", True),
+    (5, 1000, 110, 16, 128, None, "bf16", False)])
+def test_batches_beyond_whole_rounds(mss, B, L, H, K, V, heads, dtype, gradients):
+    """More blocks than find room at once: the last batches go in a launch of their own, cut finer."""
+    check(mss, inputs(B, L, H, K, V, dtype, heads=heads, lens=True, state=True, seed=B + L), gradients=gradients)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_decays_from_none_to_all(mss, dtype):
     c = inputs(2, 130, 7, 32, 32, dtype, state=True, lens=True, seed=4)
