@@ -669,7 +669,7 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
 
 // How a sequence is cut.  A block walks a segment in about the same time for every 64 steps (3.5 us with 128 keys), and a CU
 // with more than one block takes longer by what they share: measured for c blocks of eight waves 0.9 c, for four waves
-// 0.1 + 0.7 c, for 16 waves 1.3; blocks that find no room (16 waves a CU, eight in fp32) come after.  The start of a segment
+// 0.1 + 0.7 c, for 16 waves 1.3; blocks that find no room come after.  The start of a segment
 // is worth one such time.  More segments fill the CUs better but need the states between them: a pass over keys and values at
 // 0.6 (eight waves) or 0.3 (four) of the walk, and a launch.  That pass, whose blocks wait for nothing, is cut further, into
 // parts of 128 steps or more, up to a block for every CU.
@@ -680,10 +680,11 @@ struct Plan {
     int nseg, nparts, cuts;
     int64_t part_steps, cost;
 };
-int blocks_a_cu(bool bf16, int waves) { return std::max(1, (bf16 ? 16 : 8) / waves); }
+// Blocks that find room on a CU by registers and LDS: 16 waves, eight in fp32, four of them with more than 64 keys.
+int blocks_a_cu(bool bf16, int waves, int Kd) { return std::max(1, (bf16 ? 16 : Kd > 64 ? 4 : 8) / waves); }
 // blocks: of each segment; heads: whose states are wanted; waves: of a block, of one of those that make states
-Plan plan_segments(bool bf16, int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
-    const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64), most = blocks_a_cu(bf16, waves);
+Plan plan_segments(bool bf16, int Kd, int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
+    const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64), most = blocks_a_cu(bf16, waves, Kd);
     const auto time_of = [&](int64_t c) {
         return waves == 16 ? 13 * c : std::max<int64_t>(c > 0 ? 10 : 0, waves == 8 ? 9 * c : 1 + 7 * c);
     };
@@ -726,12 +727,12 @@ struct Sizes {
     }
 };
 Plan plan_walks(const Sizes& z) {
-    return plan_segments(z.bf16, z.Bt * z.outs * z.count, z.Bt * z.H * z.count, z.waves(), columns(z.Vd) / 16, z.L);
+    return plan_segments(z.bf16, z.Kd, z.Bt * z.outs * z.count, z.Bt * z.H * z.count, z.waves(), columns(z.Vd) / 16, z.L);
 }
 // Batches of a first launch: all, or as many as fill the CUs in whole rounds, when the others, cut finer, are done sooner in
 // one of their own than as the rest of a round (320 blocks of 16 waves: 182 + 64 us and 29 for the states, 327 in one launch).
 int64_t first_batches(const Sizes& z) {
-    const int64_t blocks = z.outs * z.count, room = 256 * blocks_a_cu(z.bf16, z.waves());
+    const int64_t blocks = z.outs * z.count, room = 256 * blocks_a_cu(z.bf16, z.waves(), z.Kd);
     const int64_t first = z.Bt * blocks / room * room / blocks;
     if (first < 1 || first == z.Bt) return z.Bt;
     return plan_walks(z.of(first)).cost + plan_walks(z.of(z.Bt - first)).cost + 15 < plan_walks(z).cost ? first : z.Bt;
