@@ -74,6 +74,13 @@ def token_logprobs_bwd_raw(logits, tokens, saved, dlogprobs, dentropy, dlogits, 
 
 # --------------------------------------------------------------------------------------- RMS norm
 
+def _given(*outputs):
+    """Those of a caller's outputs that there are, checked."""
+    given = [t for t in outputs if t is not None]
+    _refuse_written(*given)
+    return given
+
+
 def _norm_fwd(x, weight, residual, eps, out, residual_out, rstd, scales):
     _launch("rms_norm_fwd", x, x, residual, weight, eps, out, residual_out, rstd, scales)
 
@@ -93,13 +100,13 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-5, out=None, residual_out=None
     bfloat16.  Returns (out, residual_out): out in x's dtype, residual_out the new residual stream in residual's (None
     without residual).  residual_out=residual updates the stream in place."""
     import torch
-    given = [t for t in (out, residual_out) if t is not None]
-    _refuse_written(*given)
+    given = () if out is residual_out is None else _given(out, residual_out)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     residual_out = _stream_out(residual, residual_out)
     _norm_fwd(x, weight, residual, eps, out, residual_out, None, None)
-    _note_written(given)
+    if given:
+        _note_written(given)
     return out, residual_out
 
 
@@ -110,31 +117,31 @@ def rms_norm_fwd_e4m3(x, weight, residual=None, eps=1e-5, group=None, out=None, 
     import torch
     if group not in (None, NORM_GROUP):
         raise ValueError(f"a scale is for a row (group=None) or for {NORM_GROUP} columns, got group={group}")
-    given = [t for t in (out, scales, residual_out) if t is not None]
-    _refuse_written(*given)
+    given = () if out is scales is residual_out is None else _given(out, scales, residual_out)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        out = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
     if scales is None:
         parts = 1 if group is None else -(-x.shape[-1] // NORM_GROUP)
-        scales = torch.empty((*x.shape[:-1], parts), dtype=torch.float32, device=x.device)
+        scales = x.new_empty((*x.shape[:-1], parts), dtype=torch.float32)
     residual_out = _stream_out(residual, residual_out)
     _norm_fwd(x, weight, residual, eps, out, residual_out, None, scales)
-    _note_written(given)
+    if given:
+        _note_written(given)
     return out, scales, residual_out
 
 
 def rms_norm_fwd_save(x, weight, residual=None, eps=1e-5, out=None, residual_out=None, rstd=None):
     """rms_norm_fwd that also writes what its backward needs: returns (out, residual_out, rstd), rstd (...) float32."""
     import torch
-    given = [t for t in (out, residual_out, rstd) if t is not None]
-    _refuse_written(*given)
+    given = () if out is residual_out is rstd is None else _given(out, residual_out, rstd)
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = x.new_empty(x.shape[:-1], dtype=torch.float32)
     residual_out = _stream_out(residual, residual_out)
     _norm_fwd(x, weight, residual, eps, out, residual_out, rstd, None)
-    _note_written(given)
+    if given:
+        _note_written(given)
     return out, residual_out, rstd
 
 
@@ -188,18 +195,17 @@ def linear_attention_fwd(q, k, v, rate, scale=None, initial_state=None, seq_lens
     (None: zeros); seq_lens: (batch,) int32 on the device (None: all L; outputs past a sequence's end are 0).  Returns
     out (batch, L, heads, value_dim) in q's dtype, or (out, last_state) with last_state shaped like initial_state."""
     import torch
-    given = [t for t in (out, last_state) if t is not None]
-    _refuse_written(*given)
+    given = () if out is last_state is None else _given(out, last_state)
     if out is None:
-        out = torch.empty((*q.shape[:2], rate.shape[0], v.shape[-1]), dtype=q.dtype, device=q.device)
+        out = q.new_empty((*q.shape[:2], rate.shape[0], v.shape[-1]))
     if return_last_state and last_state is None:
-        last_state = torch.empty((q.shape[0], rate.shape[0], q.shape[-1], v.shape[-1]), dtype=torch.float32,
-                                 device=q.device)
+        last_state = q.new_empty((q.shape[0], rate.shape[0], q.shape[-1], v.shape[-1]), dtype=torch.float32)
     sizes = _attention_sizes(q, k, v, rate)
     floats = linear_attention_scratch(*sizes)[0] if sizes else 0
     _launch("linear_attention_fwd", q, q, k, v, rate, _scale_of(scale, q), initial_state, seq_lens, out,
             last_state if return_last_state else None, _scratch(floats, q.device))
-    _note_written(given)
+    if given:
+        _note_written(given)
     return (out, last_state) if return_last_state else out
 
 
@@ -211,8 +217,7 @@ def linear_attention_bwd(q, k, v, rate, dout, scale=None, initial_state=None, se
     import torch
     g = {"d" + n: torch.empty_like(t, memory_format=torch.contiguous_format) for n, t in (("q", q), ("k", k), ("v", v))}
     if return_dinitial_state:
-        g["dinitial_state"] = torch.empty((q.shape[0], rate.shape[0], q.shape[-1], v.shape[-1]), dtype=torch.float32,
-                                          device=q.device)
+        g["dinitial_state"] = q.new_empty((q.shape[0], rate.shape[0], q.shape[-1], v.shape[-1]), dtype=torch.float32)
     sizes = _attention_sizes(q, k, v, rate)
     floats = linear_attention_scratch(*sizes)[1] if sizes else 0
     _launch("linear_attention_bwd", q, q, k, v, rate, _scale_of(scale, q), initial_state, seq_lens, dout, dlast_state,
@@ -224,11 +229,10 @@ def linear_attention_update(state, q, k, v, rate, scale=None, out=None):
     """One token of linear attention (mss_linear_attention_update) on the current stream; `state`
     (batch, heads, key_dim, value_dim) float32 is updated in place.  q: (batch, q_heads, key_dim), k: (batch, k_heads,
     key_dim), v: (batch, v_heads, value_dim).  Returns out (batch, heads, value_dim) in q's dtype."""
-    import torch
     written = (state,) if out is None else (state, out)
     _refuse_written(*written)
     if out is None:
-        out = torch.empty((q.shape[0], rate.shape[0], v.shape[-1]), dtype=q.dtype, device=q.device)
+        out = q.new_empty((q.shape[0], rate.shape[0], v.shape[-1]))
     _launch("linear_attention_update", q, state, q, k, v, rate, _scale_of(scale, q), out)
     _note_written(written)
     return out
@@ -279,12 +283,12 @@ def token_logprobs_bwd(logits, tokens, saved, dlogprobs, dentropy=None, dlogits=
     """The gradient to the logits of L = sum(dlogprobs * logprobs) + sum(dentropy * entropy), on the current stream, in
     logits' dtype; saved: as token_logprobs_save returned it.  dlogits=logits writes it over them."""
     import torch
-    given = [t for t in (dlogits,) if t is not None]
-    _refuse_written(*given)
+    given = () if dlogits is None else _given(dlogits)
     if dlogits is None:
         dlogits = torch.empty_like(logits, memory_format=torch.contiguous_format)
     _launch("token_logprobs_bwd", logits, logits, tokens, saved, dlogprobs, dentropy, dlogits)
-    _note_written(given)
+    if given:
+        _note_written(given)
     return dlogits
 
 
