@@ -241,3 +241,17 @@ def test_graph_stream_bound_step_and_autograd(mss):
     out.backward(dout)
     r = mss.rms_norm_fwd_save(x, w)[2]
     assert torch.equal(x2.grad, mss.rms_norm_bwd(x, w, r, dout)["dx"])
+
+
+def test_more_rows_than_blocks(mss):
+    import torch
+    R, W = (1 << 21) + 5, 9
+    x, s = torch.randn(R, W, device="cuda"), torch.randn(R, W, device="cuda")
+    w = torch.randn(W, device="cuda")
+    out, z = mss.rms_norm_fwd(x, w, residual=s)
+    z64 = z.double()
+    assert torch.equal(z, x + s)
+    want = z64 * torch.rsqrt(z64.square().mean(-1, keepdim=True) + float(np.float32(1e-5))) * w.double()
+    assert bool(((out - want).abs() <= 20 * U * want.abs()).all())
+    q, scales, _ = mss.rms_norm_fwd_e4m3(x, w, residual=s)
+    assert bool(((q.double() * scales - want).abs() <= (2.0 ** -4 + 30 * U) * want.abs() + 2.0 ** -10 * scales).all())

@@ -239,3 +239,20 @@ def test_alternatives_of_long_rows_in_one_block(mss):
     x.zero_()
     tt = mss.token_logprobs(x, t, top=k)[3]
     assert torch.equal(tt, torch.arange(k, dtype=torch.int32, device="cuda").expand(R, k))
+
+
+def test_more_rows_than_blocks(mss):
+    import torch
+    R, V = (1 << 22) + 7, 3
+    x = torch.randn(R, V, device="cuda")
+    t = torch.randint(0, V, (R,), device="cuda", dtype=torch.int32)
+    lp, en, tl, tt = mss.token_logprobs(x, t, top=2)
+    p = torch.log_softmax(x.double(), -1)
+    want = p.gather(-1, t.long()[:, None])[:, 0]
+    assert bool(((lp - want).abs() <= 64 * U + 2 * U * want.abs()).all())
+    assert bool(((en + (p.exp() * p).sum(-1)).abs() <= 2 * 64 * U * 17).all())
+    assert torch.equal(x.gather(-1, tt.long()), x.topk(2, -1)[0])
+    _, _, saved = mss.token_logprobs_save(x, t)
+    d = mss.token_logprobs_bwd(x, t, saved, torch.ones(R, device="cuda"))
+    want = torch.nn.functional.one_hot(t.long(), V) - p.exp()
+    assert bool(((d - want).abs() <= 192 * U * (1 + p.exp())).all())
