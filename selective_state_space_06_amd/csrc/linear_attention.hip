@@ -79,8 +79,15 @@ struct AArgs {
 constexpr int kMostWalks = 3;
 struct Walks {  // of one launch: those of the same sizes side by side, so that there are blocks for every CU
     AArgs w[kMostWalks];
-    int64_t each;  // blocks of a walk
+    int64_t each;  // sets of blocks of a walk (attention_join_kernel: blocks)
+    int count;
+    int set;       // blocks of a set: neighbouring heads of a segment
 };
+// Blocks go to the eight XCDs in turn, each with an L2 of its own.  A set's blocks, which share rows of queries, keys or
+// values, go to one: 4 x 2048 x 80 heads of 128 x 64 bf16, queries and keys of 8 heads, reads 153 MB instead of 389, the
+// states of 16 heads with keys and values of 4 (f32) 65 instead of 260; the Infinity Cache had hidden most of that (450 -> 442
+// us for the former's gradients, 167 -> 163 for the latter).
+constexpr int kXcds = 8;
 
 constexpr int kFold = 8;  // more parts than these are joined by a kernel of their own
 constexpr int kChunk = 32;  // steps
@@ -186,8 +193,10 @@ constexpr int waves_wanted(bool bf16, int KD, int NW, bool states) {
 // SUB: heads of a group that a block does side by side, NW waves each, and whose outputs it sums.
 template <class E, class OUT, int KD, int NW, int SUB, bool STATES>
 __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, NW, STATES)) void attention_kernel(Walks all) {
-    const AArgs& a = all.w[blockIdx.x / all.each];
-    const int64_t block = blockIdx.x % all.each;
+    const uint32_t turn = blockIdx.x / kXcds, in_set = turn % static_cast<uint32_t>(all.set);
+    const uint32_t set = turn / static_cast<uint32_t>(all.set) * kXcds + blockIdx.x % kXcds, walk = set / static_cast<uint32_t>(all.each);
+    if (walk >= static_cast<uint32_t>(all.count)) return;  // (sets are not always a multiple of kXcds)
+    const AArgs& a = all.w[walk];
     using F = Form<E>;
     using O = typename OUT::storage;
     constexpr int C = kChunk, NP = F::NP, NS = F::NS, MT = C / 16, M2 = C / 32, KJ = KD / 32, KT = KD / 16;
@@ -215,8 +224,10 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
     auto& vs = all_vs[sub];
     auto& ps = all_ps[sub];
     const int outs = STATES ? a.H : a.outs, nseg = STATES ? a.nparts : a.nseg;
-    const int64_t b = block / nseg / outs;
-    const int o_head = static_cast<int>(block / nseg % outs), seg = static_cast<int>(block % nseg);
+    const uint32_t of_walk = set % static_cast<uint32_t>(all.each), of_seg = of_walk / static_cast<uint32_t>(nseg),
+                   sets = static_cast<uint32_t>(outs) / static_cast<uint32_t>(all.set);  // of a batch's segment
+    const int64_t b = of_seg / sets;
+    const int o_head = static_cast<int>(of_seg % sets * all.set + in_set), seg = static_cast<int>(of_walk % static_cast<uint32_t>(nseg));
     // (a group's last block may have fewer heads: the others of its waves go along with nothing)
     const int in_group = SUB > 1 ? o_head % ((a.each + SUB - 1) / SUB) * SUB + sub : 0;
     const bool there = SUB == 1 || in_group < a.each;
@@ -730,7 +741,8 @@ Plan plan_walks(const Sizes& z) {
     return plan_segments(z.bf16, z.Kd, z.Bt * z.outs * z.count, z.Bt * z.H * z.count, z.waves(), columns(z.Vd) / 16, z.L);
 }
 // Batches of a first launch: all, or as many as fill the CUs in whole rounds, when the others, cut finer, are done sooner in
-// one of their own than as the rest of a round (320 blocks of 16 waves: 182 + 64 us and 29 for the states, 327 in one launch).
+// one of their own than as the rest of a round (320 blocks of 16 waves: 182 + 64 us and
+// 29 for the states, 327 in one launch).
 int64_t first_batches(const Sizes& z) {
     const int64_t blocks = z.outs * z.count, room = 256 * blocks_a_cu(z.bf16, z.waves(), z.Kd);
     const int64_t first = z.Bt * blocks / room * room / blocks;
@@ -749,23 +761,33 @@ void walk_waves(Walks& w, int count, hipStream_t s) {
     constexpr int SUB = heads_at_once(Form<E>::NP == 1, KD, NW);
     const AArgs& a = w.w[0];
     const dim3 block(64 * NW);
-    const auto grid = [&](int64_t each) {
-        w.each = each;
-        return dim3(static_cast<unsigned>(each * count));
+    w.count = count;
+    // sets of `share` blocks, or of a divisor of it if their number would leave XCDs idle
+    const auto grid = [&](int64_t segs, int heads, int share) {
+        const auto rounded = [&](int f) { return (segs * heads / f * count + kXcds - 1) / kXcds * kXcds * f; };
+        int f = share;
+        while (f > 1 && (share % f || rounded(f) > segs * heads * count * 9 / 8)) --f;
+        w.set = f;
+        w.each = segs * heads / f;
+        return dim3(static_cast<unsigned>(rounded(f)));
     };
+    const int share_kv = a.H / std::min(a.k.heads, a.v.heads), share = std::max(share_kv, a.H / a.q.heads);
     if (a.nparts > 0) {
-        attention_kernel<E, E, KD, NW, 1, true><<<grid(a.Bt * a.H * a.nparts), block, 0, s>>>(w);
+        attention_kernel<E, E, KD, NW, 1, true><<<grid(a.Bt * a.nparts, a.H, share_kv), block, 0, s>>>(w);
         const int blocks = (a.Kd * a.Vd + 255) / 256;
-        if (a.nparts > kFold) attention_join_kernel<<<grid(a.Bt * a.H * blocks), dim3(256), 0, s>>>(w, blocks);
+        if (a.nparts > kFold) {
+            w.each = a.Bt * a.H * blocks;
+            attention_join_kernel<<<dim3(static_cast<unsigned>(w.each * count)), dim3(256), 0, s>>>(w, blocks);
+        }
     }
-    const int64_t blocks = a.Bt * a.outs * a.nseg;
     if constexpr (SUB > 1) {
         if (a.each > 1) {
-            attention_kernel<E, OUT, KD, NW, SUB, false><<<grid(blocks), dim3(64 * NW * SUB), 0, s>>>(w);
+            const int sums = (a.each + SUB - 1) / SUB;
+            attention_kernel<E, OUT, KD, NW, SUB, false><<<grid(a.Bt * a.nseg, a.outs, sums), dim3(64 * NW * SUB), 0, s>>>(w);
             return;
         }
     }
-    attention_kernel<E, OUT, KD, NW, 1, false><<<grid(blocks), block, 0, s>>>(w);
+    attention_kernel<E, OUT, KD, NW, 1, false><<<grid(a.Bt * a.nseg, a.outs, share), block, 0, s>>>(w);
 }
 // Walks of the same sizes and type of outputs, side by side, of some batches; their states in scratch.
 template <class E, class OUT>
