@@ -618,7 +618,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Walks all, int bloc
     }
 }
 
-// out (rows, groups, dim) = sum over the heads of a group of part (rows, groups, each, dim), in their order.
+// out (rows, groups, dim) = sum over the heads of a group of part (rows, groups, each, dim), in their order.  No one reads the
+// parts again: they pass the Infinity Cache by (the gradients of 4 x 2048 x 80 heads of 128 x 64 bf16, queries and keys of 8
+// heads: 441 -> 424 us).
 template <class E>
 __global__ __launch_bounds__(256) void attention_groups_kernel(const float* part, void* out, int64_t n, int each, int dim) {
     // a thread per four elements
@@ -627,7 +629,7 @@ __global__ __launch_bounds__(256) void attention_groups_kernel(const float* part
         const int c = static_cast<int>(e % (dim / 4)) * 4;
         const float* p = part + group * each * dim + c;
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int j = 0; j < each; ++j) s += *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(j) * dim);
+        for (int j = 0; j < each; ++j) s += __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(j) * dim));
         auto* o = static_cast<typename E::storage*>(out) + e * 4;
         if (sizeof(typename E::storage) == 2)
             *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
@@ -636,8 +638,11 @@ __global__ __launch_bounds__(256) void attention_groups_kernel(const float* part
 }
 
 // ---- one token.  A block per (batch, head): a thread holds four columns of every R-th row of the state; the rows'
-// parts of the output are summed through LDS.
-template <class E>
+// parts of the output are summed through LDS.  Bound by memory, the state read and written: 64 x 80 heads of 128 x 64 65 us
+// (5.1 TB/s), 59 (5.7) where the state passes the Infinity Cache by.  That is done from kPassBy bytes of it on, of which two
+// layers' do not fit the 256 MB anyway (a single state of 168 MB that does fit: 52 us, passing by 58).
+constexpr int64_t kPassBy = int64_t{1} << 27;
+template <class E, bool PASS>
 __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch a) {
     __shared__ float qk[2][kAttnMostDim];
     __shared__ float part[256 * 4];
@@ -658,14 +663,15 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
         f32x4* s = reinterpret_cast<f32x4*>(a.state + bh * a.K * a.V) + c;
 #pragma unroll 8
         for (int k = r; k < a.K; k += R) {
-            f32x4 x = s[k * quads];
+            f32x4 x = PASS ? __builtin_nontemporal_load(s + k * quads) : s[k * quads];
             const float q = qk[0][k], kk = qk[1][k];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[i] = fmaf(kk, v[i], fmaf(x[i], less, x[i]));
                 out[i] = fmaf(q, x[i], out[i]);
             }
-            s[k * quads] = x;
+            if (PASS) __builtin_nontemporal_store(x, s + k * quads);
+            else s[k * quads] = x;
         }
         *reinterpret_cast<f32x4*>(part + (r * quads + c) * 4) = out;
     }
@@ -939,8 +945,14 @@ hipError_t launch_attn_bwd(const AttnLaunch& l, hipStream_t s) {
 
 hipError_t launch_attn_update(const AttnUpdateLaunch& l, hipStream_t s) {
     const dim3 grid(static_cast<unsigned>(l.Bt * l.H)), block(256);
-    if (l.bf16) attention_update_kernel<BF16><<<grid, block, 0, s>>>(l);
-    else attention_update_kernel<F32><<<grid, block, 0, s>>>(l);
+    const bool pass = l.Bt * l.H * l.K * l.V * 4 >= kPassBy;
+    if (l.bf16) {
+        if (pass) attention_update_kernel<BF16, true><<<grid, block, 0, s>>>(l);
+        else attention_update_kernel<BF16, false><<<grid, block, 0, s>>>(l);
+    } else {
+        if (pass) attention_update_kernel<F32, true><<<grid, block, 0, s>>>(l);
+        else attention_update_kernel<F32, false><<<grid, block, 0, s>>>(l);
+    }
     return hipGetLastError();
 }
 

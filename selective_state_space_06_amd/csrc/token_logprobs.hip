@@ -365,10 +365,16 @@ struct LBArgs {
 };
 
 constexpr int kBwdWaves = 4;
+// From so many bytes of logits on, theirs and their gradients' fill the 256 MB Infinity Cache: both pass it by, and what the
+// forward left of the logits there is found (forward and gradients of 4096 x 50280 bf16 273 -> 232 us, 8192 x 8192 85 -> 78).
+// Smaller gradients stay for who reads them next.
+constexpr int64_t kPassBy = int64_t{1} << 27;
 
-template <class E, bool VEC>
+// VEC: rows are whole aligned 16-byte vectors.  PASS: kPassBy, with VEC.
+template <class E, bool VEC, bool PASS>
 __global__ __launch_bounds__(64 * kBwdWaves) void logprob_bwd_kernel(LBArgs a) {
     using S = typename E::storage;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int64_t works = a.R * a.slices, tiles = (a.V + kTile - 1) / kTile;
@@ -384,7 +390,17 @@ __global__ __launch_bounds__(64 * kBwdWaves) void logprob_bwd_kernel(LBArgs a) {
         const float h = a.h && inv != 0.0f ? a.h[row] : 0.0f;
         Raw<E> raw[2] = {};
         const auto load = [&](int64_t k, Raw<E>& r) MSS_INLINED {
-            load8<E, VEC>(p + k * kTile, a.V, clamp_tile(a.V - k * kTile), lane, r);
+            const int rem = clamp_tile(a.V - k * kTile);
+            if constexpr (PASS) {
+                const auto buffer = __builtin_amdgcn_make_buffer_rsrc(const_cast<S*>(p + k * kTile), 0,
+                                                                      rem * static_cast<int>(sizeof(S)), 0x00027000);
+#pragma unroll
+                for (int i = 0; i < kE / E::kPerVec; ++i)
+                    r.q[i] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                           buffer, lane * kE * static_cast<int>(sizeof(S)) + 16 * i, 0, 2));
+            } else {
+                load8<E, VEC>(p + k * kTile, a.V, rem, lane, r);
+            }
         };
         const auto tile = [&](int64_t k, Raw<E>& r) MSS_INLINED {
             const int rem = clamp_tile(a.V - k * kTile);
@@ -403,7 +419,16 @@ __global__ __launch_bounds__(64 * kBwdWaves) void logprob_bwd_kernel(LBArgs a) {
                 for (int e = 0; e < kE; ++e)
                     if (e == mine) v[e] += g;
             }
-            store8<E, VEC>(o + k * kTile, rem, lane, v);
+            if constexpr (PASS) {
+#pragma unroll
+                for (int j = 0; j < kE / E::kPerVec; ++j) {
+                    const int at = lane * kE + j * E::kPerVec;
+                    const uint4 w = E::pack(v + j * E::kPerVec);
+                    if (at < rem) __builtin_nontemporal_store(u32x4{w.x, w.y, w.z, w.w}, reinterpret_cast<u32x4*>(o + k * kTile + at));
+                }
+            } else {
+                store8<E, VEC>(o + k * kTile, rem, lane, v);
+            }
         };
         const int64_t lo = from + wave;
         if (lo < to) load(lo, raw[0]);
@@ -462,12 +487,15 @@ hipError_t launch_logprob_bwd(const LogprobBwdLaunch& l, hipStream_t s) {
     a.tiles = (tiles + n - 1) / n;
     a.slices = static_cast<int>((tiles + a.tiles - 1) / a.tiles);
     const dim3 grid(blocks_for(l.R * a.slices, 1)), block(64 * kBwdWaves);
+    const bool pass = l.vec_ok && l.R * l.V * (l.bf16 ? 2 : 4) >= kPassBy;
     if (l.bf16) {
-        if (l.vec_ok) logprob_bwd_kernel<BF16, true><<<grid, block, 0, s>>>(a);
-        else logprob_bwd_kernel<BF16, false><<<grid, block, 0, s>>>(a);
+        if (pass) logprob_bwd_kernel<BF16, true, true><<<grid, block, 0, s>>>(a);
+        else if (l.vec_ok) logprob_bwd_kernel<BF16, true, false><<<grid, block, 0, s>>>(a);
+        else logprob_bwd_kernel<BF16, false, false><<<grid, block, 0, s>>>(a);
     } else {
-        if (l.vec_ok) logprob_bwd_kernel<F32, true><<<grid, block, 0, s>>>(a);
-        else logprob_bwd_kernel<F32, false><<<grid, block, 0, s>>>(a);
+        if (pass) logprob_bwd_kernel<F32, true, true><<<grid, block, 0, s>>>(a);
+        else if (l.vec_ok) logprob_bwd_kernel<F32, true, false><<<grid, block, 0, s>>>(a);
+        else logprob_bwd_kernel<F32, false, false><<<grid, block, 0, s>>>(a);
     }
     return hipGetLastError();
 }

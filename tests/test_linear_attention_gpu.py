@@ -211,6 +211,25 @@ def test_one_token_chain_is_the_sequence(mss, B, H, K, V, heads, dtype):
     assert torch.equal(s2, state)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_token_of_many_states(mss, dtype):
+    """States too large for the cache have the bits of the same states in parts."""
+    import torch
+    B, H, K, V = 37, 128, 64, 112
+    tt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    state = torch.randn(B, H, K, V, device="cuda")
+    assert state.numel() * 4 > 1 << 27
+    q, k, v = (torch.randn(B, h, d, device="cuda").to(tt) for h, d in ((8, K), (H, K), (32, V)))
+    rate = torch.rand(H, device="cuda")
+    parts, outs = [], []
+    for i in range(0, B, 5):
+        s = state[i:i + 5].clone()
+        outs.append(mss.linear_attention_update(s, q[i:i + 5], k[i:i + 5], v[i:i + 5], rate))
+        parts.append(s)
+    out = mss.linear_attention_update(state, q, k, v, rate)
+    assert torch.equal(out, torch.cat(outs)) and torch.equal(state, torch.cat(parts))
+
+
 def test_one_token_with_extreme_decays(mss):
     import torch
     S = torch.randn(1, 3, 16, 16, device="cuda")

@@ -256,3 +256,25 @@ def test_more_rows_than_blocks(mss):
     d = mss.token_logprobs_bwd(x, t, saved, torch.ones(R, device="cuda"))
     want = torch.nn.functional.one_hot(t.long(), V) - p.exp()
     assert bool(((d - want).abs() <= 192 * U * (1 + p.exp())).all())
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 50280), ("bf16", 50281), ("f32", 25004)])
+def test_gradients_larger_than_the_cache(mss, dtype, V):
+    """Rows that are and are not whole vectors, of more logits than are kept for the next reader; also in place."""
+    import torch
+    R = 1400
+    x = (torch.randn(R, V, device="cuda") * 2.5).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    assert x.numel() * x.element_size() > 1 << 27
+    rows = [0, 1, 701, R - 1]
+    t = torch.randint(0, V, (R,), device="cuda", dtype=torch.int32)
+    g, h = torch.randn(R, device="cuda"), torch.randn(R, device="cuda")
+    _, _, saved = mss.token_logprobs_save(x, t)
+    d = mss.token_logprobs_bwd(x, t, saved, g, h)
+    xr, n = host64(x[rows]).astype(np.float32), V / 2048 + 1
+    ref, M = oracle.token_logprobs_bwd(xr, t[rows].cpu().numpy(), g[rows].cpu().numpy(), h[rows].cpu().numpy())
+    p = np.exp(xr - xr.max(-1, keepdims=True), dtype=np.float64)
+    p /= p.sum(-1, keepdims=True)
+    lim = (190 + 2 * n) * U * (M + np.abs(h[rows].cpu().numpy())[:, None] * p) + (2.0 ** -8 if dtype == "bf16" else 0.0) * np.abs(ref)
+    close(d[rows], ref, lim + 1e-37, "dlogits")
+    mss.token_logprobs_bwd(x, t, saved, g, h, dlogits=x)
+    assert torch.equal(x, d)
