@@ -10,10 +10,10 @@
 //     dx_v = g (1[v = token] - p_v) - h p_v (log p_v + entropy),
 // one pass over the logits from the row's m, 1 / s and entropy - log s.
 //
-// Both are bound by memory where there is enough of it: 4096 x 50280 bf16 79 us forward (5.2 TB/s), 151 backward
-// (5.5 TB/s).  A batch of 128 x 128007 bf16 takes 13 us without alternatives (2.5 TB/s; 6.4 at the rate of a copy, the rest is the
-// ends of two launches), 18 with 5 of them and 23 with 20; as lists kept by every wave along its way 14, 23 and 39.  One row of
-// 50277 f32 with 20 alternatives takes 15 us, mostly latencies in a row: launches, loads, merges.
+// Both are bound by memory where there is enough of it: 4096 x 50280 bf16 80 us forward (5.2 TB/s), 230 with the gradient
+// (5.4 TB/s).  A batch of 128 x 128007 bf16 takes 14 us without alternatives (2.4 TB/s; 6.4 at the rate of a copy, the rest is
+// the ends of two launches), 19 with 5 of them and 23 with 20; as lists kept by every wave along its way 14, 23 and 39.  One row
+// of 50277 f32 with 20 alternatives takes 13 us, mostly latencies in a row: launches, loads, merges.
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -76,12 +76,31 @@ __device__ __forceinline__ void join_lanes(Sums& v, int count) {
 // The k greatest of two sorted lists, `other` held the other way round (entry j in lane size - 1 - j): the greater of each
 // pair of entries, which rises and falls, sorted by comparing lanes ever closer to each other.  size: list_size(k).
 __device__ __forceinline__ int list_size(int k) { return k > 1 ? 1 << (32 - __builtin_clz(k - 1)) : 1; }
+template <int X>
+__device__ __forceinline__ uint32_t across(uint32_t v) {  // v of the lane X away
+    const int i = static_cast<int>(v);
+    if (X == 1) return __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, true);   // quad_perm 1 0 3 2
+    if (X == 2) return __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, true);   // quad_perm 2 3 0 1
+    if (X == 4)                                                                   // row_half_mirror, quad_perm 3 2 1 0
+        return __builtin_amdgcn_update_dpp(0, __builtin_amdgcn_update_dpp(0, i, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true);
+    if (X == 8) return __builtin_amdgcn_update_dpp(0, i, 0x128, 0xF, 0xF, true);  // row_ror 8
+    if (X == 16) return __builtin_amdgcn_ds_swizzle(i, 16 << 10 | 0x1F);
+    return __shfl_xor(i, X);
+}
+template <int X>
+__device__ __forceinline__ void compare_across(uint64_t& key, int size, int lane) {
+    if (X >= size) return;
+    const uint64_t o = join64(across<X>(static_cast<uint32_t>(key >> 32)), across<X>(static_cast<uint32_t>(key)));
+    key = (o > key) == ((lane & X) == 0) ? o : key;
+}
 __device__ __forceinline__ uint64_t merge_two(uint64_t key, uint64_t other, int size, int lane) {
     key = other > key ? other : key;
-    for (int x = size / 2; x > 0; x >>= 1) {
-        const uint64_t o = __shfl_xor(key, x);
-        key = (o > key) == ((lane & x) == 0) ? o : key;
-    }
+    compare_across<32>(key, size, lane);
+    compare_across<16>(key, size, lane);
+    compare_across<8>(key, size, lane);
+    compare_across<4>(key, size, lane);
+    compare_across<2>(key, size, lane);
+    compare_across<1>(key, size, lane);
     return key;
 }
 // Joins the lists of W waves into wave 0's (lanes from k on hold kNone).  Every wave comes here.
@@ -342,12 +361,13 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_join_kernel(LArgs a) {
     }
 }
 
-// Four blocks for every CU, each wave with a tile or more; at most 64 slices.  (128 x 128007 bf16 with 5 alternatives: two
-// blocks for every CU 19 us, four 18, eight 22; blocks of eight waves 19.)
+// Four blocks for every CU, each wave with two tiles or more (one row of 50277 f32 with 20 alternatives: one tile 13.5 us, two
+// 12.9); at most 64 slices.  (128 x 128007 bf16 with 5 alternatives: two blocks for every CU 19 us, four 18, eight 22; blocks of
+// eight waves 19.)
 void plan_logprob(int64_t R, int64_t V, int64_t* per, int* slices) {
     const int64_t tiles = (V + kTile - 1) / kTile;
     int64_t n = (1024 + R - 1) / R;
-    n = std::max<int64_t>(1, std::min({n, (tiles + kWaves - 1) / kWaves, int64_t{64}}));
+    n = std::max<int64_t>(1, std::min({n, (tiles + 2 * kWaves - 1) / (2 * kWaves), int64_t{64}}));
     *per = (tiles + n - 1) / n;
     *slices = static_cast<int>((tiles + *per - 1) / *per);
 }
