@@ -13,7 +13,7 @@
 // Both are bound by memory where there is enough of it: 4096 x 50280 bf16 80 us forward (5.2 TB/s), 230 with the gradient
 // (5.4 TB/s).  A batch of 128 x 128007 bf16 takes 14 us without alternatives (2.4 TB/s; 6.4 at the rate of a copy, the rest is
 // the ends of two launches), 19 with 5 of them and 23 with 20; as lists kept by every wave along its way 14, 23 and 39.  One row
-// of 50277 f32 with 20 alternatives takes 13 us, mostly latencies in a row: launches, loads, merges.
+// of 50277 f32 with 20 alternatives takes 14 us, mostly latencies in a row: launches, loads, merges.
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -147,20 +147,20 @@ __device__ __forceinline__ void finish_row(const LArgs& a, int64_t row, float gi
     }
 }
 
-// One block per (row, slice of the vocabulary), its waves on successive tiles in turn, kAhead of them on their way, by
+// One block of W waves per (row, slice of the vocabulary), its waves on successive tiles in turn, kAhead of them on their way, by
 // loads that are not branched around (past the end they give 0).  Which lane takes which logit does not depend on where the
 // row lies, so that equal rows have equal results: rows of any alignment are loaded as they are (4096 x 50277 bf16: 101 us
 // with branches, 92 without).
-constexpr int kWaves = 4, kAhead = 2;
+constexpr int kWaves = 4, kMostWaves = 16, kAhead = 2;
 
-template <class E, bool TOP>
-__global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
+template <class E, bool TOP, int W>
+__global__ __launch_bounds__(64 * W) void logprob_kernel(LArgs a) {
     using S = typename E::storage;
     constexpr int ES = sizeof(S);
-    __shared__ uint64_t all[TOP ? kWaves * 64 : 1];
-    __shared__ double all_s[kWaves], all_t[kWaves];
-    __shared__ float all_m[kWaves];
-    __shared__ uint32_t bars[2][kWaves];
+    __shared__ uint64_t all[TOP ? W * 64 : 1];
+    __shared__ double all_s[W], all_t[W];
+    __shared__ float all_m[W];
+    __shared__ uint32_t bars[2][W];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int64_t works = a.R * a.slices;
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
             if (ES == 2 && rem & 1) settle8<E, false>(a.V, rem, lane, r);
             float v[kE];
             r.unpack(v);
-            load(k + kAhead * kWaves, r);
+            load(k + kAhead * W, r);
             if (k >= to) return;
             if (rem < kTile) {
 #pragma unroll
@@ -218,18 +218,18 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
         };
         const int64_t lo = from + wave;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) load(lo + i * kWaves, raw[i]);
+        for (int i = 0; i < kAhead; ++i) load(lo + i * W, raw[i]);
         const float given = a.slices == 1 && wave == 0 ? logit_of_token<E>(a, row) : 0.0f;
-        for (int64_t k = lo; k < to; k += kAhead * kWaves) {
+        for (int64_t k = lo; k < to; k += kAhead * W) {
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i) tile(k + i * kWaves, raw[i]);
+            for (int i = 0; i < kAhead; ++i) tile(k + i * W, raw[i]);
         }
         uint64_t key = kNone;
         if constexpr (TOP) {
             // the alternatives are at least as great as the k-th greatest of any wave's lanes, and as the least of the
-            // waves' (k / kWaves)-th greatest
+            // waves' (k / W)-th greatest
             const uint32_t most = order_of(m);
-            const int share = (a.K + kWaves - 1) / kWaves;
+            const int share = (a.K + W - 1) / W;
             uint32_t kth = 0, part = 0;
 #pragma unroll
             for (int bit = 31; bit >= 16; --bit) {
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
             {
                 uint32_t least = ~0u;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
+                for (int w = 0; w < W; ++w) {
                     bar = bars[0][w] > bar ? bars[0][w] : bar;
                     least = bars[1][w] < least ? bars[1][w] : least;
                 }
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
                 }
             };
             // the tiles of the lanes that have such logits again, 64 vectors of them at a time
-            const int mine = lo < to ? static_cast<int>((to - lo + kWaves - 1) / kWaves) : 0;
+            const int mine = lo < to ? static_cast<int>((to - lo + W - 1) / W) : 0;
             int lg = 0;
             while (lg < 6 && 1 << lg < mine) ++lg;
             const int first_token = static_cast<int>(lo * kTile);
@@ -271,7 +271,7 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
                 const int src = __shfl(order, lane >> lg);
                 for (int base = 0; base < mine; base += 64) {
                     const int i = base + (lane & ((1 << lg) - 1));
-                    const int64_t at = (lo + static_cast<int64_t>(i) * kWaves) * kTile + src * kE;
+                    const int64_t at = (lo + static_cast<int64_t>(i) * W) * kTile + src * kE;
                     const bool in = lane >> lg < count && i < mine;
                     const int n = !in || at >= a.V ? 0 : a.V - at < kE ? static_cast<int>(a.V - at) : kE;  // of this lane's
                     float v[kE];
@@ -301,11 +301,11 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_kernel(LArgs a) {
             all_s[wave] = v.s;
             all_t[wave] = v.t;
         }
-        if (TOP) join_lists<kWaves>(all, key, a.K, wave, lane);
+        if (TOP) join_lists<W>(all, key, a.K, wave, lane);
         else __syncthreads();
         if (wave == 0) {
-            v = lane < kWaves ? Sums{all_m[lane], all_s[lane], all_t[lane]} : Sums{-INFINITY, 0.0, 0.0};
-            join_lanes(v, kWaves);
+            v = lane < W ? Sums{all_m[lane], all_s[lane], all_t[lane]} : Sums{-INFINITY, 0.0, 0.0};
+            join_lanes(v, W);
             if (a.slices == 1) {
                 finish_row(a, row, given, v, key, lane);
             } else {
@@ -361,11 +361,21 @@ __global__ __launch_bounds__(64 * kWaves) void logprob_join_kernel(LArgs a) {
     }
 }
 
-// Four blocks for every CU, each wave with two tiles or more (one row of 50277 f32 with 20 alternatives: one tile 13.5 us, two
-// 12.9); at most 64 slices.  (128 x 128007 bf16 with 5 alternatives: two blocks for every CU 19 us, four 18, eight 22; blocks of
-// eight waves 19.)
-void plan_logprob(int64_t R, int64_t V, int64_t* per, int* slices) {
+// A row to a block of 16 waves where rows are no more than CUs and a wave has at most eight tiles: one launch, without scratch
+// (128 x 32000 f32 with 20 alternatives: 14.4 us, 16.5 in slices; 16 x 32000 13.8 and 13.1, 1 x 50277 13.8 and 13.0, where the
+// second launch, 5 us of the caller's time, costs more; 400 x 5000 23 and 16).
+// Otherwise four blocks of four waves for every CU, each wave with two tiles or more (one row of 50277 f32 with 20
+// alternatives: one tile 13.5 us, two 12.9); at most 64 slices.  (128 x 128007 bf16 with 5 alternatives: two blocks for every
+// CU 19 us, four 18, eight 22; blocks of eight waves 19.)
+void plan_logprob(int64_t R, int64_t V, int64_t* per, int* slices, int* waves) {
     const int64_t tiles = (V + kTile - 1) / kTile;
+    *waves = kWaves;
+    if (R <= 256 && tiles > 2 * kWaves && tiles <= 8 * kMostWaves) {
+        *per = tiles;
+        *slices = 1;
+        *waves = kMostWaves;
+        return;
+    }
     int64_t n = (1024 + R - 1) / R;
     n = std::max<int64_t>(1, std::min({n, (tiles + 2 * kWaves - 1) / (2 * kWaves), int64_t{64}}));
     *per = (tiles + n - 1) / n;
@@ -465,8 +475,8 @@ __global__ __launch_bounds__(64 * kBwdWaves) void logprob_bwd_kernel(LBArgs a) {
 int64_t logprob_scratch(int64_t R, int64_t V, int64_t K) {
     if (R == 0) return 0;
     int64_t per;
-    int slices;
-    plan_logprob(R, V, &per, &slices);
+    int slices, waves;
+    plan_logprob(R, V, &per, &slices, &waves);
     return slices == 1 ? 0 : R * slices * (5 + 2 * K);
 }
 
@@ -475,20 +485,27 @@ hipError_t launch_logprob_fwd(const LogprobLaunch& l, hipStream_t s) {
     a.logits = l.logits; a.tokens = l.tokens; a.logprobs = l.logprobs; a.entropy = l.entropy;
     a.top_logprobs = l.top_logprobs; a.top_tokens = l.top_tokens; a.saved = l.saved;
     a.R = l.R; a.V = l.V; a.K = l.K;
-    plan_logprob(l.R, l.V, &a.tiles, &a.slices);
+    int waves;
+    plan_logprob(l.R, l.V, &a.tiles, &a.slices, &waves);
     const int64_t works = l.R * a.slices;
     a.part_s = reinterpret_cast<double*>(l.scratch);
     a.part_t = a.part_s + works;
     a.cand = reinterpret_cast<uint64_t*>(a.part_t + works);
     a.part_m = reinterpret_cast<float*>(a.cand + works * l.K);
     const dim3 grid(blocks_for(works, 1)), block(64 * kWaves);
-    if (l.bf16) {
-        if (l.K) logprob_kernel<BF16, true><<<grid, block, 0, s>>>(a);
-        else logprob_kernel<BF16, false><<<grid, block, 0, s>>>(a);
-    } else {
-        if (l.K) logprob_kernel<F32, true><<<grid, block, 0, s>>>(a);
-        else logprob_kernel<F32, false><<<grid, block, 0, s>>>(a);
-    }
+    const auto go = [&](auto e) {
+        using E = decltype(e);
+        const dim3 wide(64 * kMostWaves);
+        if (l.K) {
+            if (waves == kWaves) logprob_kernel<E, true, kWaves><<<grid, block, 0, s>>>(a);
+            else logprob_kernel<E, true, kMostWaves><<<grid, wide, 0, s>>>(a);
+        } else {
+            if (waves == kWaves) logprob_kernel<E, false, kWaves><<<grid, block, 0, s>>>(a);
+            else logprob_kernel<E, false, kMostWaves><<<grid, wide, 0, s>>>(a);
+        }
+    };
+    if (l.bf16) go(BF16{});
+    else go(F32{});
     if (a.slices > 1) {
         const dim3 rows(blocks_for(l.R, 1));
         if (l.bf16) logprob_join_kernel<BF16><<<rows, block, 0, s>>>(a);

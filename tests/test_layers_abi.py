@@ -47,7 +47,7 @@ def strided(t):
     return Tensor.make(t.data, t.dtype, s, st)
 
 
-B, L, W, H, Q, KH, VH, K, V, NV = 2, 70, 300, 8, 2, 4, 8, 32, 48, 20000
+B, L, W, H, Q, KH, VH, K, V, NV = 2, 70, 300, 8, 2, 4, 8, 32, 48, 70000
 
 
 def norm_args(dt=MSS_BF16):
