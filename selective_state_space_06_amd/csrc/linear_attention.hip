@@ -291,30 +291,45 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         rows(k_at, k_bytes, k_off, QR, rk);
         rows(v_at, v_bytes, v_off, VR, rv);
     };
-    const auto put = [&](const Raw<E>& r, int plane, auto write) MSS_INLINED {
+    // Powers of the decay.  A score's lane is a step t = 16 tb + r16, its rows are s = 16 ta + 4 g + i.
+    const float rate = fminf(fmaxf(a.rate[h], 0.0f), kMostRate), rl = rate * kLog2e;
+    const auto power = [&](int n) MSS_INLINED { return fast_exp2(-rl * static_cast<float>(n)); };
+    // fp32 values that only enter the state are weighed where they are cut into parts, not joined, weighed and cut again
+    // (1 x 32768 x 16 heads of 64 x 64: 163 -> 157 us).
+    constexpr bool kWeighed = STATES && NP > 1;
+    float weights[kWeighed ? NV : 1];
+    if constexpr (kWeighed) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) weights[j] = power(C - 1 - v_row - j * VR) * a.s_add;
+    }
+    const auto put = [&](const Raw<E>& r, float weight, int plane, auto write) MSS_INLINED {
         if constexpr (NP == 1) {
             write(r.q[0], 0);
         } else {
             float x[kE];
             r.unpack(x);
+            if constexpr (kWeighed) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) x[e] *= weight;
+            }
             s16x8 part[NP];
             cut<NP>(x, part);
 #pragma unroll
             for (int n = 0; n < NP; ++n) write(__builtin_bit_cast(uint4, part[n]), n * plane);
         }
     };
-    const auto put8 = [&](const Raw<E>& r, uint16_t* p, int plane) MSS_INLINED {
-        put(r, plane, [&](uint4 q, int to) MSS_INLINED { *reinterpret_cast<uint4*>(p + to) = q; });
+    const auto put8 = [&](const Raw<E>& r, uint16_t* p, int plane, float weight = 1.0f) MSS_INLINED {
+        put(r, weight, plane, [&](uint4 q, int to) MSS_INLINED { *reinterpret_cast<uint4*>(p + to) = q; });
     };
     const auto put4 = [&](const Raw<E>& r, uint16_t* lo, uint16_t* hi, int plane) MSS_INLINED {
-        put(r, plane, [&](uint4 q, int to) MSS_INLINED {
+        put(r, 1.0f, plane, [&](uint4 q, int to) MSS_INLINED {
             *reinterpret_cast<uint2*>(lo + to) = make_uint2(q.x, q.y);
             *reinterpret_cast<uint2*>(hi + to) = make_uint2(q.z, q.w);
         });
     };
     const auto key_at = [](int row, int col) MSS_INLINED { return col ^ (row & 8) >> 1 ^ (row & 4) << 2; };
     const auto value_at = [](int row, int col) MSS_INLINED { return col ^ (row & 8) * (VT / 32); };
-    const auto store = [&]() MSS_INLINED {
+    const auto store = [&](int n) MSS_INLINED {
         if (QR <= C || q_row < C) {
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
@@ -324,7 +339,12 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
             }
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) put8(rv[j], &vs[0][v_row + j * VR][value_at(v_row + j * VR, v_col)], C * VS);
+        for (int j = 0; j < NV; ++j) {
+            const int row = v_row + j * VR;
+            float weight = 1.0f;
+            if constexpr (kWeighed) weight = n == C ? weights[j] : power(n - 1 - row > 0 ? n - 1 - row : 0) * a.s_add;
+            put8(rv[j], &vs[0][row][value_at(row, v_col)], C * VS, weight);
+        }
     };
     // eight values of a column, rows 32 m + 8 g ...
     const auto read_values = [&](int m, s16x8* f) MSS_INLINED {
@@ -335,9 +355,6 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         }
     };
 
-    // Powers of the decay.  A score's lane is a step t = 16 tb + r16, its rows are s = 16 ta + 4 g + i.
-    const float rate = fminf(fmaxf(a.rate[h], 0.0f), kMostRate), rl = rate * kLog2e;
-    const auto power = [&](int n) MSS_INLINED { return fast_exp2(-rl * static_cast<float>(n)); };
     const auto uniform = [](float x) MSS_INLINED {
         return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
     };
@@ -416,7 +433,7 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
     float faded = since * power(1 - early);
     for (int at = 0; at < todo; at += C) {
         const int n = rows_at(at), ahead = rows_at(at + C);
-        store();
+        store(n);
         move(q_at, q_bytes, ahead);
         move(k_at, k_bytes, ahead);
         move(v_at, v_bytes, ahead);
@@ -515,25 +532,30 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
                 for (int i = 0; i < 4; ++i) st[j][i] = fmaf(st[j][i], gone, st[j][i]);
 #pragma unroll
             for (int m = 0; m < M2; ++m) {
-                float w[8], x[8];
+                s16x8 wf[3];
+                if constexpr (kWeighed) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = (m + 1 < M2 ? tail * tail32 : tail) * small[7 - e];
-                if (n < C) {  // rows past the end are zeros
+                    for (int p = 0; p < 3; ++p) wf[p] = vf[m][p];
+                } else {
+                    float w[8], x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = (m + 1 < M2 ? tail * tail32 : tail) * small[7 - e];
+                    if (n < C) {  // rows past the end are zeros
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const int s = n - 1 - (32 * m + 8 * g + e);
+                            w[e] = power(s > 0 ? s : 0) * a.s_add;
+                        }
+                    }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int s = n - 1 - (32 * m + 8 * g + e);
-                        w[e] = power(s > 0 ? s : 0) * a.s_add;
+                        x[e] = bf16_to_f32(static_cast<uint16_t>(vf[m][0][e]));
+#pragma unroll
+                        for (int p = 1; p < NP; ++p) x[e] += bf16_to_f32(static_cast<uint16_t>(vf[m][p][e]));
+                        x[e] *= w[e];
                     }
+                    cut<3>(x, wf);
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = bf16_to_f32(static_cast<uint16_t>(vf[m][0][e]));
-#pragma unroll
-                    for (int p = 1; p < NP; ++p) x[e] += bf16_to_f32(static_cast<uint16_t>(vf[m][p][e]));
-                    x[e] *= w[e];
-                }
-                s16x8 wf[3];
-                cut<3>(x, wf);
                 constexpr int G = NP == 1 && SUB == 4 ? 2 : 4;  // tiles at once
 #pragma unroll
                 for (int j0 = 0; j0 < KT; j0 += G) {
