@@ -170,14 +170,16 @@ def rms_norm_bwd(z, weight, rstd, dout, dresidual_out=None, return_dresidual=Non
 
 # ------------------------------------------------------------------------------- linear attention
 
-def _attention_sizes(q, k, v, rate):
-    """The scratch query's sizes; None for shapes that the call itself refuses, with its own status."""
-    if not (q.ndim == k.ndim == v.ndim == 4 and rate.ndim == 1):
-        return None
-    sizes = (q.shape[0], q.shape[1], rate.shape[0], q.shape[2], k.shape[2], v.shape[2], q.shape[3], v.shape[3])
-    heads, (K, V) = sizes[2:6], sizes[6:]
-    ok = all(h >= 1 and heads[0] % h == 0 for h in heads) and all(1 <= d <= 128 and d % 16 == 0 for d in (K, V))
-    return sizes if ok else None
+def _attention_floats(q, k, v, rate):
+    """Floats of scratch of the forward and of the backward; none for what the call itself refuses, with its own status."""
+    if q.ndim == 4 and k.ndim == 4 and v.ndim == 4 and rate.ndim == 1:
+        batch, L, q_heads, key_dim = q.shape
+        _, _, v_heads, value_dim = v.shape
+        st, fwd, bwd = _native().linear_attention_scratch(batch, L, rate.shape[0], q_heads, k.shape[2], v_heads, key_dim,
+                                                          value_dim)
+        if st == 0:
+            return fwd, bwd
+    return 0, 0
 
 
 def _scale_of(scale, q):
@@ -200,8 +202,7 @@ def linear_attention_fwd(q, k, v, rate, scale=None, initial_state=None, seq_lens
         out = q.new_empty((*q.shape[:2], rate.shape[0], v.shape[-1]))
     if return_last_state and last_state is None:
         last_state = q.new_empty((q.shape[0], rate.shape[0], q.shape[-1], v.shape[-1]), dtype=torch.float32)
-    sizes = _attention_sizes(q, k, v, rate)
-    floats = linear_attention_scratch(*sizes)[0] if sizes else 0
+    floats, _ = _attention_floats(q, k, v, rate)
     _launch("linear_attention_fwd", q, q, k, v, rate, _scale_of(scale, q), initial_state, seq_lens, out,
             last_state if return_last_state else None, _scratch(floats, q.device))
     if given:
@@ -218,8 +219,7 @@ def linear_attention_bwd(q, k, v, rate, dout, scale=None, initial_state=None, se
     g = {"d" + n: torch.empty_like(t, memory_format=torch.contiguous_format) for n, t in (("q", q), ("k", k), ("v", v))}
     if return_dinitial_state:
         g["dinitial_state"] = q.new_empty((q.shape[0], rate.shape[0], q.shape[-1], v.shape[-1]), dtype=torch.float32)
-    sizes = _attention_sizes(q, k, v, rate)
-    floats = linear_attention_scratch(*sizes)[1] if sizes else 0
+    _, floats = _attention_floats(q, k, v, rate)
     _launch("linear_attention_bwd", q, q, k, v, rate, _scale_of(scale, q), initial_state, seq_lens, dout, dlast_state,
             g["dq"], g["dk"], g["dv"], g.get("dinitial_state"), _scratch(floats, q.device))
     return g
