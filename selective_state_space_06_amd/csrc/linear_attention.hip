@@ -18,15 +18,16 @@
 // next product's operand as it stands, when the other operand's rows are taken in the same order, and what has to be
 // turned is read from LDS by the instruction that turns.
 //
-// What bounds it: neither memory nor the matrix cores, but the instructions of a chunk and their waits, 2.2 us for 32 steps
-// with 128 x 128 state, of which decaying the state, cutting it into parts and reading it turned are most.  So what counts
-// is blocks on a CU at once: chunks of 64 steps have twice the scores' work and fewer fit, chunks of 16 leave half of the
-// matrix instruction empty.  A long sequence with few heads is cut into
-// segments; the states between them come from a pass over keys and values alone, whose parts are added up by the block that
-// reads them (up to eight) or by a kernel of their own.
+// What bounds it: neither memory nor the matrix cores, but the instructions of a chunk and their waits, 2.4 us for 32 steps
+// with 128 x 128 state (272 VALU instructions a wave, 45 of them MFMA, 75 SALU, 37 LDS), of which decaying the state, cutting
+// it into parts and reading keys turned are most.  So what counts is instructions, and blocks on a CU at once: chunks of 64
+// steps have twice the scores' work and fewer fit, chunks of 16 leave half of the matrix instruction empty.  A long sequence
+// with few heads is cut into segments; the states between them come from a pass over keys and values alone, whose parts are
+// added up by the block that reads them (up to eight) or by a kernel of their own.
 // The gradients of shared heads are sums over the heads of a group: a block does as many of them side by side as 16 waves
 // hold and adds the outputs up in LDS, in their order; what is left goes through memory and attention_groups_kernel
-// (4 x 2048 x 80 heads, of queries and keys 8: 553 us for the three gradients, 600 with all through memory).
+// (4 x 2048 x 80 heads, of queries and keys 8, when this was built: 553 us for the three gradients, 600 with all through
+// memory).
 //
 // bf16 products of fp32 values: a value is cut into bf16 parts (hi = bf16(x), mid = bf16(x - hi), ...), each exact,
 // and the products of parts that matter are summed in fp32.  bf16 inputs are one part; states and scores, met by a
@@ -34,9 +35,9 @@
 // fp32 inputs are three parts everywhere, with the six products down to 2^-24 (2.7 times the rate of the fp32 matrix
 // instruction).
 //
-// Measured, with both types' own sizes: 4 x 2048 x 32 heads of 128 x 128 bf16 109 us (2.5 TB/s, 158 TFLOP/s of the formula's
-// products); 1 x 32768 x 16 heads of 64 x 64 f32 197 us, of them states 64 and their sums 19; output and gradients of
-// 4 x 2048 x 80 heads of 128 x 64 bf16 with queries and keys of 8 heads 689 us, of 3 x 1531 x 12 heads of 64 x 96 f32 204.
+// Measured: 4 x 2048 x 32 heads of 128 x 128 bf16 97 us (2.9 TB/s, 178 TFLOP/s of the formula's products), of them states 23;
+// 1 x 32768 x 16 heads of 64 x 64 f32, keys and values of 4, 156 us, of them states 49 and their sums 8; output and gradients of
+// 4 x 2048 x 80 heads of 128 x 64 bf16 with queries and keys of 8 heads 548 us, of 3 x 1531 x 12 heads of 64 x 96 f32 167.
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -186,7 +187,7 @@ __device__ __forceinline__ float part_decay(const AArgs& a, float rate, int64_t 
 
 // Waves a SIMD that a kernel's registers leave room for: as many as its LDS does.
 constexpr int waves_wanted(bool bf16, int KD, int NW, bool states) {
-    return bf16 ? 4 : KD == 128 && NW == 4 ? (states ? 2 : 1) : states && KD == 64 ? 4 : 2;
+    return bf16 ? 4 : !states && KD == 64 && NW == 4 ? 3 : KD == 128 && NW == 4 ? (states ? 2 : 1) : states && KD == 64 ? 4 : 2;
 }
 
 // STATES: only the state that a part of a segment adds, from zero.  OUT: the outputs' type.  NW: waves, 16 columns each.
@@ -205,7 +206,10 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
     // lie an odd multiple of eight banks apart (1 KB in 4.4 cycles; 8.4 at four banks).  Rows read turned, and rows of both
     // uses, also have their columns moved by bits of the row (key_at, value_at), so that the eight rows of 16 columns that 32
     // lanes read turned, and the 16 rows of 4 that they read for scores, meet in no bank.
-    constexpr int QS = KD + 16, KS = KD + 32, VS = VT + 16, PS = C + 16;
+    // (fp32 with 64 keys and four waves: rows close enough for three blocks on a CU; the gradients of 4 x 2048 x 24 heads of
+    // 64 x 64 177 -> 169 us.)
+    constexpr bool kClose = NP == 3 && KD == 64 && NW == 4;
+    constexpr int QS = KD + 16, KS = kClose ? KD + 16 : KD + 32, VS = VT + 16, PS = kClose ? C + 8 : C + 16;
     constexpr int QU = KD / 8, VU = VT / 8;                  // units of eight elements a row
     constexpr int QR = T / QU, VR = T / VU;                  // rows that the block loads at once
     constexpr int NQ = C > QR ? C / QR : 1, NV = C / VR;     // (f32 with 64 keys: half of eight waves load them)
