@@ -712,13 +712,14 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
 
 // How a sequence is cut.  A block walks a segment in about the same time for every 64 steps (3.5 us with 128 keys), and a CU
 // with more than one block takes longer by what they share: measured for c blocks of eight waves 0.9 c, for four waves
-// 0.1 + 0.7 c, for 16 waves 1.3; blocks that find no room come after.  The start of a segment
-// is worth one such time.  More segments fill the CUs better but need the states between them: a pass over keys and values at
-// 0.6 (eight waves) or 0.3 (four) of the walk, and a launch.  That pass, whose blocks wait for nothing, is cut further, into
-// parts of 128 steps or more, up to a block for every CU.
+// 0.1 + 0.7 c, for 16 waves 1.3; blocks that find no room come after.  The start of a segment is worth one such time.  More
+// segments (at most 128) fill the CUs better but need the states between them: a pass over keys and values at 0.6 (eight
+// waves) or 0.3 (four) of the walk, and a launch; and then to be added up, a microsecond a part of 128 x 128 state in the
+// blocks that read them, or in a launch more.  The pass, whose blocks wait for nothing, is cut further, into parts of 128
+// steps or more, up to a block for every CU.
 // Times by the number of segments, the one that is taken in brackets: 4 x 2048 x 32 heads of 128 x 128 bf16, 1 to 4: 121,
 // [104], 113, 120 us; 4 x 2048 x 80 of 128 x 64 bf16: 127, 125, [117], 128; 3 x 1531 x 12 of 64 x 96 f32, 4, 6, 8, 16: 55,
-// [51], 66, 53; 1 x 2048 x 32 of 128 x 128 bf16, keys and values of 8 heads, 4, 6, 8, 16: 65, 60, [55], 56.
+// [51], 66, 53; 1 x 2048 x 32 of 128 x 128 bf16, keys and values of 8 heads, 4, 6, 8, 16: 65, 60, 55, [56].
 struct Plan {
     int nseg, nparts, cuts;
     int64_t part_steps, cost;
@@ -726,17 +727,20 @@ struct Plan {
 // Blocks that find room on a CU by registers and LDS: 16 waves, eight in fp32, four of them with more than 64 keys.
 int blocks_a_cu(bool bf16, int waves, int Kd) { return std::max(1, (bf16 ? 16 : Kd > 64 ? 4 : 8) / waves); }
 // blocks: of each segment; heads: whose states are wanted; waves: of a block, of one of those that make states
-Plan plan_segments(bool bf16, int Kd, int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
+Plan plan_segments(bool bf16, int Kd, int Vd, int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
     const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64), most = blocks_a_cu(bf16, waves, Kd);
     const auto time_of = [&](int64_t c) {
         return waves == 16 ? 13 * c : std::max<int64_t>(c > 0 ? 10 : 0, waves == 8 ? 9 * c : 1 + 7 * c);
     };
     int64_t best = 0, segment = steps64;
-    for (int64_t n = 1; n <= std::min<int64_t>(64, steps64 / 2 + 1); ++n) {
+    for (int64_t n = 1; n <= std::min<int64_t>(128, steps64); ++n) {
         const int64_t each = (steps64 + n - 1) / n, segs = (steps64 + each - 1) / each;  // of 64 steps, and how many there are
         const int64_t c = (blocks * segs + 255) / 256;
         int64_t cost = (c / most * time_of(most) + (c % most ? time_of(c % most) : 0)) * (each + 1);
-        if (segs > 1) cost += (state_waves == 8 ? 6 : 3) * heads * (segs - 1) * each / 256 + 15;
+        if (segs > 1) {
+            cost += (state_waves == 8 ? 6 : 3) * heads * (segs - 1) * each / 256 + 15;
+            cost += segs - 1 <= kFold ? 3 * (segs - 1) * Kd * Vd / (128 * 128) : 15;
+        }
         if (n == 1 || cost < best) best = cost, segment = each;
     }
     Plan p;
@@ -770,7 +774,7 @@ struct Sizes {
     }
 };
 Plan plan_walks(const Sizes& z) {
-    return plan_segments(z.bf16, z.Kd, z.Bt * z.outs * z.count, z.Bt * z.H * z.count, z.waves(), columns(z.Vd) / 16, z.L);
+    return plan_segments(z.bf16, z.Kd, z.Vd, z.Bt * z.outs * z.count, z.Bt * z.H * z.count, z.waves(), columns(z.Vd) / 16, z.L);
 }
 // Batches of a first launch: all, or as many as fill the CUs in whole rounds, when the others, cut finer, are done sooner in
 // one of their own than as the rest of a round (320 blocks of 16 waves: 182 + 64 us and
