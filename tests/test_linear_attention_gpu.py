@@ -123,6 +123,13 @@ def test_few_heads_cut_in_segments(mss, B, L, H, K, V, lens, dtype):
     check(mss, inputs(B, L, H, K, V, dtype, lens=lens, state=True, seed=L))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_one_head_in_many_segments(mss, dtype):
+    """More segments than a wave has lanes, whose parts are joined by a kernel of their own."""
+    check(mss, inputs(1, 12345, 1, 16, 32, dtype, state=True, seed=12))
+    check(mss, inputs(2, 9000, 1, 32, 16, dtype, lens=True, state=True, seed=13))
+
+
 @pytest.mark.parametrize("B,L,H,K,V,heads,dtype,gradients", [
     (11, 500, 40, 16, 16, (4, 4, 40), "bf16", True), (7, 500, 40, 16, 16, (4, 4, 40), "f32", True),
     (5, 1000, 110, 16, 128, None, "bf16", False)])
