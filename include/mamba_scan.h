@@ -519,7 +519,7 @@ int mss_beam_reorder(const mss_tensor_t* const* states, int count, const mss_ten
  * RMS norm with the residual stream's addition, the step in front of a layer.  Per row of width W:
  *     z = x + residual  (rounded to the stream's type: what residual_out holds and the norm is of; x without residual)
  *     rstd = 1 / sqrt(mean(z^2) + eps),   out = z rstd weight
- * and in 8 bits (out of MSS_F8E4M3) out = (z rstd weight) / scale rounded to nearest even, with
+ * and in 8 bits (out of MSS_F8E4M3) out = (z rstd weight) / scale, the fp32 quotient rounded to nearest even, with
  * scale = max(max |z rstd weight|, 2^-100) / 448 over the row, or over each 128 columns of it: out scale is the value.
  *   x             (..., W)   f32 or bf16, 2 to 4 dimensions
  *   residual      (..., W)   f32 or bf16, nullable

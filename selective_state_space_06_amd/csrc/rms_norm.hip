@@ -120,7 +120,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void rms_fwd_kernel(NArgs a) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
-            for (int e = 0; e < kE; ++e) z[j][e] *= r * w[j][e];
+            for (int e = 0; e < kE; ++e) z[j][e] = z[j][e] * r * w[j][e];
         if constexpr (!F8) {
             auto* o = static_cast<typename X::storage*>(a.out) + row * W;
 #pragma unroll
@@ -156,13 +156,21 @@ __global__ __launch_bounds__(64 * kMostWaves) void rms_fwd_kernel(NArgs a) {
                 } else if ((lane & 15) == 0 && lane * kE < rem[j]) {
                     a.scales[row * a.G + at[j] / 128 + (lane >> 4)] = scale;
                 }
+                // The quotients z / scale as fp32 has them, at most 448: the product with the reciprocal and what it lacks,
+                // put back.  The product alone has a rounding too many: next to the middle between two 8-bit values it
+                // falls on the other side.
                 const float inv = 1.0f / scale;
                 int q[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {  // round to nearest even; |z inv| is at most 448 and a rounding
+                for (int e = 0; e < kE; ++e) {
+                    const float near = z[j][e] * inv;
+                    z[j][e] = fmaf(fmaf(-near, scale, z[j][e]), inv, near);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // round to nearest even
                     const float* v = z[j] + 4 * h;
-                    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, 0, false);
-                    q[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, lo, true);
+                    const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+                    q[h] = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
                 }
                 const int t0 = lane * kE;
                 uint8_t* p = o + at[j] + t0;
