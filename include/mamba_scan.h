@@ -573,7 +573,7 @@ int mss_rms_norm_bwd(const mss_tensor_t* z, const mss_tensor_t* weight, const ms
  * batch times heads at most 2^20 and L below 2^31 (MSS_ERR_UNSUPPORTED otherwise).  All but rate and seq_lens are
  * 16-byte aligned (MSS_ERR_LAYOUT).  No output may overlap an input or another output.
  * Computed in chunks of 32 steps on the matrix cores; the state is fp32.  bf16 inputs are taken as they are,
- * states and scores to 2^-17, what enters the state to 2^-25; f32 inputs, whose size is below 3.38e38, in three bf16
+ * states, scores and what enters the state to 2^-25; f32 inputs, whose size is below 3.38e38, in three bf16
  * parts, products to 2^-24.  An infinity or a NaN in a chunk may reach all its outputs, those before it among them, and
  * all later ones.
  */
