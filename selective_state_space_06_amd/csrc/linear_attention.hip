@@ -93,7 +93,7 @@ constexpr int kXcds = 8;
 
 constexpr int kFold = 8;  // more parts than these are joined by a kernel of their own
 constexpr int kChunk = 32;  // steps
-constexpr float kMostRate = 1e30f;  // beyond it l^n is 0 for every n but 0, which 0 times infinity would not be
+constexpr float kMostRate = 200.0f;  // from there on l^n is 0 in fp32 for every n but 0, also for a rate of infinity
 
 __device__ __forceinline__ f32x4 mma(s16x8 a, s16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
@@ -178,12 +178,33 @@ __device__ __forceinline__ void mma_each(A a, B b, f32x4* c) {
 // The LDS reads before this are issued before what comes after it (the compiler would issue each in front of its use).
 __device__ __forceinline__ void issue_reads() { __builtin_amdgcn_sched_barrier(0); }
 
-// l^n - 1 for the steps n that a state decays by in part i of a sequence of len steps.
-__device__ __forceinline__ float part_decay(const AArgs& a, float rate, int64_t len, int i) {
+// e^-(d + lost) for a small lost: exp2 of t = -d log2 e as it is rounded, then what t lacks, to three roundings for every d.
+// (exp2 of the rounded product alone is off by d roundings.)
+constexpr float kLn2Rest = -1.90465421e-9f;  // ln 2 - kLn2
+__device__ __forceinline__ float power_of(float d, float lost) {
+    const float t = d * -kLog2e, e = fast_exp2(t);
+    return fmaf(e, fmaf(-t, kLn2Rest, fmaf(-t, kLn2, -d)) - lost, e);
+}
+// What a state decays by in some steps: l^n where that is under 1/2, l^n - 1 otherwise.  Near 1 the power's own rounding would be
+// the same for every chunk and add up; far from 1 a rounding of l^n - 1 is one of the undecayed state, and 6% of what is left
+// at a rate of 1/2 and 32 steps.
+struct Decay {
+    float by;
+    int whole;  // by is l^n itself
+};
+__device__ __forceinline__ float decayed(float x, Decay d) { return d.whole ? x * d.by : fmaf(x, d.by, x); }
+__device__ __forceinline__ Decay decay_of(float d, float lost) {
+    const bool whole = d > kLn2;
+    return {whole ? power_of(d, lost) : expm1f(-d), whole};
+}
+// Of the steps that a state decays by in part i of a sequence of len steps.
+__device__ __forceinline__ Decay part_decay(const AArgs& a, float rate, int64_t len, int i) {
     int64_t n = len - i * a.part_steps;
     n = n < 0 ? 0 : n < a.part_steps ? n : a.part_steps;
     if (n > 0 && i == 0 && a.back) --n;
-    return expm1f(-rate * static_cast<float>(n));
+    const double exact = static_cast<double>(rate) * static_cast<double>(n);
+    const float d = static_cast<float>(exact);
+    return decay_of(d, static_cast<float>(exact - d));
 }
 
 // Waves a SIMD that a kernel's registers leave room for: as many as its LDS does.
@@ -297,8 +318,11 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         rows(v_at, v_bytes, v_off, VR, rv);
     };
     // Powers of the decay.  A score's lane is a step t = 16 tb + r16, its rows are s = 16 ta + 4 g + i.
-    const float rate = fminf(fmaxf(a.rate[h], 0.0f), kMostRate), rl = rate * kLog2e;
-    const auto power = [&](int n) MSS_INLINED { return fast_exp2(-rl * static_cast<float>(n)); };
+    const float rate = fminf(fmaxf(a.rate[h], 0.0f), kMostRate);
+    const auto power = [&](int n) MSS_INLINED {
+        const float steps = static_cast<float>(n), d = rate * steps;
+        return power_of(d, fmaf(rate, steps, -d));
+    };
     // fp32 values that only enter the state are weighed where they are cut into parts, not joined, weighed and cut again
     // (1 x 32768 x 16 heads of 64 x 64: 163 -> 157 us).
     constexpr bool kWeighed = STATES && NP > 1;
@@ -376,7 +400,19 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         decay[i] = power(steps > 0 ? steps : 0) * (a.s_add * a.s_out);
     }
     const float since = power(r16) * a.s_out, tail = power(24 - 8 * g) * a.s_add, step16 = uniform(power(16));
-    const float tail32 = uniform(power(32)), less = uniform(expm1f(-rate * C));
+    const float tail32 = uniform(power(32));
+    const auto decay_over = [&](int n) MSS_INLINED {  // the same for all lanes
+        const float steps = static_cast<float>(n), d = rate * steps;
+        const Decay gone = decay_of(d, fmaf(rate, steps, -d));
+        return Decay{uniform(gone.by), __builtin_amdgcn_readfirstlane(gone.whole)};
+    };
+    // l^C as a float and what that lacks.  Chunks decay by the float; what it lacks is owed, and goes into the factor of a
+    // later chunk once it is a step of it: a rounding that is the same for every chunk would add up.  (A branch between the two
+    // forms of Decay parts the factors from the products behind them: 4 x 2048 x 32 heads of 128 x 128 bf16 3% slower.)
+    const Decay of_chunk = decay_over(C);
+    const float chunk_kept = of_chunk.whole ? of_chunk.by : 1.0f + of_chunk.by;
+    const float chunk_rest = of_chunk.whole ? 0.0f : of_chunk.by - (chunk_kept - 1.0f);
+    float owed = 0.0f;
     // The state: tile j holds rows 32 (j / 2) + 8 g + 4 (j % 2) + i of a column, so that two tiles are eight rows in turn.
     f32x4 st[KT];
     const int64_t per = static_cast<int64_t>(a.Kd) * a.Vd;
@@ -411,9 +447,9 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         const bool joined = a.nparts > kFold && seg > 0;
         for (int i = joined ? seg * a.cuts - 1 : -1; i < seg * a.cuts; ++i) {
             const float* p = i < 0 ? a.init + bh * per : a.parts + (bh * a.nparts + i) * per;
-            const float gone = i < 0 || joined ? 0.0f : part_decay(a, rate, len, i);
+            const Decay gone = i < 0 || joined ? Decay{0.0f, 0} : part_decay(a, rate, len, i);
             if (i >= 0 || a.init)
-                each_of_state(i < 0 && a.turned, [&](float x, int j) MSS_INLINED { return fmaf(x, gone, x) + p[j]; });
+                each_of_state(i < 0 && a.turned, [&](float x, int j) MSS_INLINED { return decayed(x, gone) + p[j]; });
         }
         // scores behind a step stay 0: only the others are written
         for (int e = tid; e < NS * C * PS / 8; e += T) reinterpret_cast<uint4*>(&ps[0][0][0])[e] = make_uint4(0, 0, 0, 0);
@@ -530,11 +566,19 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
         }
         // the state after the chunk, if it is read
         if (STATES || ahead || keep) {
-            const float gone = n - early == C ? less : expm1f(-rate * static_cast<float>(n - early));
+            float kept;  // l^n
+            if (n - early == C) {
+                owed += chunk_rest;
+                kept = chunk_kept + owed;
+                owed -= kept - chunk_kept;
+            } else {
+                const Decay gone = decay_over(n - early);
+                kept = gone.whole ? gone.by : 1.0f + gone.by;
+            }
 #pragma unroll
             for (int j = 0; j < KT; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) st[j][i] = fmaf(st[j][i], gone, st[j][i]);
+                for (int i = 0; i < 4; ++i) st[j][i] *= kept;
 #pragma unroll
             for (int m = 0; m < M2; ++m) {
                 s16x8 wf[3];
@@ -613,7 +657,7 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
 // The states that enter the segments but the first, from what the parts add, in place (in the last part of the segment
 // before): a block per (batch, head) and 256 elements.  The parts' decays are made once for the block, not by every thread.
 __global__ __launch_bounds__(256) void attention_join_kernel(Walks all, int blocks) {
-    __shared__ float gone[256];
+    __shared__ Decay gone[256];
     const AArgs& a = all.w[blockIdx.x / all.each];
     const int64_t block = blockIdx.x % all.each, bh = block / blocks, b = bh / a.H;
     const int per = a.Kd * a.Vd, x = static_cast<int>(block % blocks) * 256 + threadIdx.x;
@@ -636,7 +680,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Walks all, int bloc
 #pragma unroll
         for (int i = 0; i < G; ++i) {
             if (i0 + i >= a.nparts) break;
-            s = fmaf(s, gone[(i0 + i) % 256], s) + adds[i];
+            s = decayed(s, gone[(i0 + i) % 256]) + adds[i];
             if (--left == 0) {
                 left = a.cuts;
                 if (x < per) o[static_cast<int64_t>(i0 + i) * per] = s;
@@ -680,7 +724,7 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
         qk[0][tid] = E::load1(a.q, (b * a.Hq + h / (a.H / a.Hq)) * a.K + tid) * a.scale;
         qk[1][tid] = E::load1(a.k, (b * a.Hk + h / (a.H / a.Hk)) * a.K + tid);
     }
-    const float less = expm1f(-fminf(fmaxf(a.rate[h], 0.0f), kMostRate));
+    const Decay gone = decay_of(fminf(fmaxf(a.rate[h], 0.0f), kMostRate), 0.0f);
     f32x4 v, out = {0.0f, 0.0f, 0.0f, 0.0f};
     const int64_t at = (b * a.Hv + h / (a.H / a.Hv)) * a.V + 4 * c;
 #pragma unroll
@@ -694,7 +738,7 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
             const float q = qk[0][k], kk = qk[1][k];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                x[i] = fmaf(kk, v[i], fmaf(x[i], less, x[i]));
+                x[i] = fmaf(kk, v[i], decayed(x[i], gone));
                 out[i] = fmaf(q, x[i], out[i]);
             }
             if (PASS) __builtin_nontemporal_store(x, s + k * quads);
