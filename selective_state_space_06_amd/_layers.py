@@ -339,6 +339,12 @@ class LinearAttentionFunction:
         return _function("attention", _make_attention).apply(q, k, v, rate, scale, initial_state, seq_lens)
 
 
+def _aligned(t):
+    """t dense and 16-byte aligned: a gradient that autograd delivers may be a view of another at any element."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() % 16 else t
+
+
 def _make_attention():
     import torch
 
@@ -354,8 +360,8 @@ def _make_attention():
         @torch.autograd.function.once_differentiable
         def backward(ctx, dout, dlast):
             q, k, v, rate, initial_state, seq_lens = ctx.saved_tensors
-            g = linear_attention_bwd(q, k, v, rate, dout.contiguous(), scale=ctx.scale, initial_state=initial_state,
-                                     seq_lens=seq_lens, dlast_state=dlast.contiguous(),
+            g = linear_attention_bwd(q, k, v, rate, _aligned(dout), scale=ctx.scale, initial_state=initial_state,
+                                     seq_lens=seq_lens, dlast_state=_aligned(dlast),
                                      return_dinitial_state=initial_state is not None)
             return g["dq"], g["dk"], g["dv"], None, None, g.get("dinitial_state"), None
 
