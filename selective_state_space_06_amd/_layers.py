@@ -145,16 +145,17 @@ def rms_norm_fwd_save(x, weight, residual=None, eps=1e-5, out=None, residual_out
     return out, residual_out, rstd
 
 
-def rms_norm_bwd(z, weight, rstd, dout, dresidual_out=None, return_dresidual=None):
+def rms_norm_bwd(z, weight, rstd, dout, dresidual_out=None, return_dresidual=None, return_dweight=True):
     """Gradients of rms_norm_fwd for L = sum(dout * out) + sum(dresidual_out * residual_out), on the current stream.
     z: the forward's residual_out, or its x without residual; rstd: as rms_norm_fwd_save wrote it.  Returns a dict: dx
-    in dout's dtype, dweight (width,) float32 and, with return_dresidual (None: when dresidual_out is given), dresidual
-    in z's dtype (the same tensor as dx where that is dout's)."""
+    in dout's dtype, dweight (width,) float32 (unless return_dweight is false) and, with return_dresidual (None: when
+    dresidual_out is given), dresidual in z's dtype (the same tensor as dx where that is dout's)."""
     import torch
     if return_dresidual is None:
         return_dresidual = dresidual_out is not None
-    g = dict(dx=torch.empty_like(dout, memory_format=torch.contiguous_format),
-             dweight=torch.empty_like(weight, memory_format=torch.contiguous_format))
+    g = dict(dx=torch.empty_like(dout, memory_format=torch.contiguous_format))
+    if return_dweight:
+        g["dweight"] = torch.empty_like(weight, memory_format=torch.contiguous_format)
     own = None
     if return_dresidual:
         if z.dtype != dout.dtype:
@@ -162,8 +163,8 @@ def rms_norm_bwd(z, weight, rstd, dout, dresidual_out=None, return_dresidual=Non
         g["dresidual"] = g["dx"] if own is None else own
     # sizes that the query refuses are refused by the call itself, with its own status
     width = z.shape[-1] if z.ndim else 0
-    floats = rms_norm_bwd_scratch(z.numel() // width, width) if 1 <= width <= 16384 else 0
-    _launch("rms_norm_bwd", z, z, weight, rstd, dout, dresidual_out, g["dx"], own, g["dweight"],
+    floats = rms_norm_bwd_scratch(z.numel() // width, width) if return_dweight and 1 <= width <= 16384 else 0
+    _launch("rms_norm_bwd", z, z, weight, rstd, dout, dresidual_out, g["dx"], own, g.get("dweight"),
             _scratch(floats, z.device))
     return g
 
@@ -293,6 +294,13 @@ def token_logprobs_bwd(logits, tokens, saved, dlogprobs, dentropy=None, dlogits=
 
 
 # ---------------------------------------------------------------------------------------- autograd
+#
+# An output that is not used has no gradient (None), which the library takes as 0 where it is not the main one; what an input
+# that needs no gradient would have is not made where the library can leave it out.
+
+def _dense(grad):
+    return None if grad is None else grad.contiguous()
+
 
 class RMSNormFunction:
     """torch.autograd wrapper of the RMS norm: RMSNormFunction.apply(x, weight, residual, eps) -> (out, residual_out),
@@ -312,16 +320,18 @@ def _make_norm():
         def forward(ctx, x, weight, residual, eps):
             out, stream, rstd = rms_norm_fwd_save(x, weight, residual=residual, eps=eps)
             ctx.save_for_backward(x if stream is None else stream, weight, rstd)
-            ctx.has_stream = stream is not None
+            ctx.set_materialize_grads(False)
+            ctx.dtype = x.dtype
             return out, stream
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dout, dstream):
             z, weight, rstd = ctx.saved_tensors
-            g = rms_norm_bwd(z, weight, rstd, dout.contiguous(),
-                             dresidual_out=dstream.contiguous() if ctx.has_stream else None)
-            return g["dx"], g["dweight"], g.get("dresidual"), None
+            dout = z.new_zeros(z.shape, dtype=ctx.dtype) if dout is None else dout.contiguous()
+            g = rms_norm_bwd(z, weight, rstd, dout, dresidual_out=_dense(dstream),
+                             return_dresidual=ctx.needs_input_grad[2], return_dweight=ctx.needs_input_grad[1])
+            return g["dx"], g.get("dweight"), g.get("dresidual"), None
 
     return _Norm
 
@@ -340,9 +350,8 @@ class LinearAttentionFunction:
 
 
 def _aligned(t):
-    """t dense and 16-byte aligned: a gradient that autograd delivers may be a view of another at any element."""
-    t = t.contiguous()
-    return t.clone() if t.data_ptr() % 16 else t
+    """t (dense, or None) 16-byte aligned: a gradient that autograd delivers may be a view of another at any element."""
+    return t.clone() if t is not None and t.data_ptr() % 16 else t
 
 
 def _make_attention():
@@ -353,16 +362,18 @@ def _make_attention():
         def forward(ctx, q, k, v, rate, scale, initial_state, seq_lens):
             out, last = linear_attention_fwd(q, k, v, rate, scale=scale, initial_state=initial_state, seq_lens=seq_lens)
             ctx.save_for_backward(q, k, v, rate, initial_state, seq_lens)
-            ctx.scale = scale
+            ctx.set_materialize_grads(False)
+            ctx.scale, ctx.shape = scale, out.shape
             return out, last
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dout, dlast):
             q, k, v, rate, initial_state, seq_lens = ctx.saved_tensors
-            g = linear_attention_bwd(q, k, v, rate, _aligned(dout), scale=ctx.scale, initial_state=initial_state,
-                                     seq_lens=seq_lens, dlast_state=_aligned(dlast),
-                                     return_dinitial_state=initial_state is not None)
+            dout = q.new_zeros(ctx.shape) if dout is None else _aligned(dout.contiguous())
+            g = linear_attention_bwd(q, k, v, rate, dout, scale=ctx.scale, initial_state=initial_state,
+                                     seq_lens=seq_lens, dlast_state=_aligned(_dense(dlast)),
+                                     return_dinitial_state=ctx.needs_input_grad[5])
             return g["dq"], g["dk"], g["dv"], None, None, g.get("dinitial_state"), None
 
     return _Attention
@@ -385,13 +396,16 @@ def _make_logprobs():
         def forward(ctx, logits, tokens):
             logprobs, entropy, saved = token_logprobs_save(logits, tokens)
             ctx.save_for_backward(logits, tokens, saved)
+            ctx.set_materialize_grads(False)
             return logprobs, entropy
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dlogprobs, dentropy):
             logits, tokens, saved = ctx.saved_tensors
-            return token_logprobs_bwd(logits, tokens, saved, dlogprobs.contiguous(), dentropy.contiguous()), None
+            if dlogprobs is None:
+                dlogprobs = saved.new_zeros(tokens.shape)
+            return token_logprobs_bwd(logits, tokens, saved, dlogprobs.contiguous(), _dense(dentropy)), None
 
     return _Logprobs
 
