@@ -545,7 +545,7 @@ int mss_rms_norm_fwd(const mss_tensor_t* x, const mss_tensor_t* residual, const 
  *   dresidual_out  (..., W)   dtype of z, nullable
  *   dx             (..., W)   dtype of dout, written: dL/dz
  *   dresidual      (..., W)   dtype of z, nullable, written: dL/dz too (where z has dout's type, dx is both)
- *   dweight        (W,)       f32, nullable, written (sum over rows in fp32, fixed order); scratch with it alone
+ *   dweight        (W,)       f32, nullable, written (sum over rows in 64 bits, fixed order); scratch with it alone
  * No output may overlap an input or another output.
  */
 int mss_rms_norm_bwd_scratch(int64_t rows, int64_t width, int64_t* floats);

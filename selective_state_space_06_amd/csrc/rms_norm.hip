@@ -7,8 +7,8 @@
 // registers (its waves on successive tiles of 512 columns, eight to a lane) between the sum and the outputs.  Forward, a
 // block per row: 8192 x 4096 bf16 47.8 us (5.6 TB/s), into 8 bits with a scale per row 44.9 (5.2 TB/s), 8192 x 2560 bf16 with
 // the stream in fp32 48.5 (5.2 TB/s); blocks that keep their weights and go over rows in turn 50.0, 50.3 and 51.4, and no
-// better with the next row on its way.  Backward, a block goes over rows in turn and keeps its sums of dw, which a second
-// kernel joins in a fixed order: 6123 x 2049 f32, forward and backward, 84 us (4.8 TB/s).
+// better with the next row on its way.  Backward, a block goes over rows in turn and keeps its sums of dw, in 64 bits and
+// rounded once; a second kernel joins them in a fixed order, in 64 bits too: 6123 x 2049 f32, forward and backward, 84 us (4.8 TB/s).
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -204,26 +204,31 @@ struct NBArgs {
 template <class X, class S, bool VEC, int NT>
 __global__ __launch_bounds__(64 * kMostWaves) void rms_bwd_kernel(NBArgs a) {
     __shared__ float parts[2][kMostWaves];
-    const int lane = threadIdx.x & 63;
+    const int own_lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x >> 6));
     const int waves = blockDim.x >> 6;
     const int64_t W = a.W;
     int rem[NT];
     int64_t at[NT];
-    float w[NT][kE], dw[NT][kE] = {};
+    float w[NT][kE];
+    double dw[NT][kE] = {};  // over many rows: 64 bits
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         at[j] = static_cast<int64_t>(wave + j * waves) * kTile;
         rem[j] = clamp_tile(W - at[j]);
         Raw<F32> q{};
         if (rem[j] > 0) {
-            load8<F32, false>(a.w + at[j], W, rem[j], lane, q);
-            settle8<F32, false>(W, rem[j], lane, q);
+            load8<F32, false>(a.w + at[j], W, rem[j], own_lane, q);
+            settle8<F32, false>(W, rem[j], own_lane, q);
         }
         q.unpack(w[j]);
     }
     int turn = 0;
     for (int64_t row = blockIdx.x; row < a.R; row += gridDim.x, turn ^= 1) {
+        // Rows that are no whole vectors: what a lane's place comes to in the last one is made for each row, not kept in
+        // registers, of which two tiles leave none (1599 x 10001 bf16 with z in f32, forward and gradients: 156 -> 121 us).
+        int lane = own_lane;
+        if (!VEC && NT > 1) asm("" : "+v"(lane));
         const auto* zp = static_cast<const typename S::storage*>(a.z) + row * W;
         const auto* dp = static_cast<const typename X::storage*>(a.dy) + row * W;
         Raw<S> rz[NT] = {}, rr[NT] = {};
@@ -253,7 +258,7 @@ __global__ __launch_bounds__(64 * kMostWaves) void rms_bwd_kernel(NBArgs a) {
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
                 z[j][e] *= r;
-                dw[j][e] = fmaf(d[j][e], z[j][e], dw[j][e]);
+                dw[j][e] += d[j][e] * z[j][e];
                 d[j][e] *= w[j][e];
                 sum = fmaf(d[j][e], z[j][e], sum);
             }
@@ -275,15 +280,20 @@ __global__ __launch_bounds__(64 * kMostWaves) void rms_bwd_kernel(NBArgs a) {
     if (!a.part) return;
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-        if (rem[j] > 0) store8<F32, false>(a.part + blockIdx.x * W + at[j], rem[j], lane, dw[j]);
+        if (rem[j] > 0) {
+            float part[kE];
+#pragma unroll
+            for (int e = 0; e < kE; ++e) part[e] = static_cast<float>(dw[j][e]);
+            store8<F32, false>(a.part + blockIdx.x * W + at[j], rem[j], own_lane, part);
+        }
 }
 
-// dw[c] = sum of part[p][c] over p: 16 columns a block, 64 threads to a column, joined in a fixed order.
+// dw[c] = sum of part[p][c] over p, in 64 bits: 16 columns a block, 64 threads to a column, joined in a fixed order.
 __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* part, int64_t P, int64_t W, float* dw) {
-    __shared__ float s[64][17];
+    __shared__ double s[64][17];
     const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
     const int64_t col = blockIdx.x * 16ll + c;
-    float v = 0.0f;
+    double v = 0.0;
     if (col < W)
 #pragma unroll 8
         for (int64_t p = g; p < P; p += 64) v += part[p * W + col];
@@ -293,7 +303,7 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* part, int64_t
         if (g < h) s[g][c] += s[g + h][c];
         __syncthreads();
     }
-    if (g == 0 && col < W) dw[col] = s[0][c];
+    if (g == 0 && col < W) dw[col] = static_cast<float>(s[0][c]);
 }
 
 // Waves a block and tiles a wave for rows of W columns.  One tile a wave as long as 16 waves reach: 8192 x 8192 bf16 92 us, 97
