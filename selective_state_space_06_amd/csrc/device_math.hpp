@@ -20,6 +20,14 @@ __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_ex
 __device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
 __device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
 
+// e^(x + rest) for a finite x and a small rest, to three roundings whatever x is: exp2 of t = x log2 e as it is rounded, then
+// what t lacks.  (exp2 of the rounded product alone is off by up to |x| roundings.)
+constexpr float kLn2Rest = -1.90465421e-9f;  // ln 2 - kLn2
+__device__ __forceinline__ float exact_exp(float x, float rest = 0.0f) {
+    const float t = x * kLog2e, e = fast_exp2(t);
+    return fmaf(e, fmaf(-t, kLn2Rest, fmaf(-t, kLn2, x)) + rest, e);
+}
+
 // softplus(x) = log(1 + e^x) = max(x, 0) + log1p(w), w = e^-|x| in (0, 1].
 // log1p(w) is taken as log(s) - ((s - 1) - w) with s = fl(1 + w): s - 1 is exact for
 // s in [1, 2], so (s - 1) - w is exactly the rounding error e of s, and

@@ -178,13 +178,6 @@ __device__ __forceinline__ void mma_each(A a, B b, f32x4* c) {
 // The LDS reads before this are issued before what comes after it (the compiler would issue each in front of its use).
 __device__ __forceinline__ void issue_reads() { __builtin_amdgcn_sched_barrier(0); }
 
-// e^-(d + lost) for a small lost: exp2 of t = -d log2 e as it is rounded, then what t lacks, to three roundings for every d.
-// (exp2 of the rounded product alone is off by d roundings.)
-constexpr float kLn2Rest = -1.90465421e-9f;  // ln 2 - kLn2
-__device__ __forceinline__ float power_of(float d, float lost) {
-    const float t = d * -kLog2e, e = fast_exp2(t);
-    return fmaf(e, fmaf(-t, kLn2Rest, fmaf(-t, kLn2, -d)) - lost, e);
-}
 // What a state decays by in some steps: l^n where that is under 1/2, l^n - 1 otherwise.  Near 1 the power's own rounding would be
 // the same for every chunk and add up; far from 1 a rounding of l^n - 1 is one of the undecayed state, and 6% of what is left
 // at a rate of 1/2 and 32 steps.
@@ -195,7 +188,7 @@ struct Decay {
 __device__ __forceinline__ float decayed(float x, Decay d) { return d.whole ? x * d.by : fmaf(x, d.by, x); }
 __device__ __forceinline__ Decay decay_of(float d, float lost) {
     const bool whole = d > kLn2;
-    return {whole ? power_of(d, lost) : expm1f(-d), whole};
+    return {whole ? exact_exp(-d, -lost) : expm1f(-d), whole};
 }
 // Of the steps that a state decays by in part i of a sequence of len steps.
 __device__ __forceinline__ Decay part_decay(const AArgs& a, float rate, int64_t len, int i) {
@@ -321,7 +314,7 @@ __global__ __launch_bounds__(64 * NW * SUB, waves_wanted(Form<E>::NP == 1, KD, N
     const float rate = fminf(fmaxf(a.rate[h], 0.0f), kMostRate);
     const auto power = [&](int n) MSS_INLINED {
         const float steps = static_cast<float>(n), d = rate * steps;
-        return power_of(d, fmaf(rate, steps, -d));
+        return exact_exp(-d, -fmaf(rate, steps, -d));
     };
     // fp32 values that only enter the state are weighed where they are cut into parts, not joined, weighed and cut again
     // (1 x 32768 x 16 heads of 64 x 64: 163 -> 157 us).
