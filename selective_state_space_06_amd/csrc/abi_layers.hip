@@ -127,7 +127,7 @@ int mss_rms_norm_bwd(const mss_tensor_t* z, const mss_tensor_t* weight, const ms
         mss::NormBwdLaunch a;
         a.z = z->data; a.weight = static_cast<const float*>(weight->data); a.rstd = static_cast<const float*>(rstd->data);
         a.dout = dout->data; a.dresidual_out = ptr<const void>(dresidual_out); a.dx = dx->data;
-        a.dresidual = ptr<void>(dresidual); a.dweight = ptr<float>(dweight); a.scratch = ptr<float>(scratch);
+        a.dresidual = ptr<void>(dresidual); a.dweight = ptr<float>(dweight); a.scratch = dweight ? ptr<float>(scratch) : nullptr;
         a.R = R; a.W = W;
         a.x_bf16 = dout->dtype == MSS_BF16; a.z_bf16 = z->dtype == MSS_BF16;
         a.vec_ok = whole_vectors(W, z->dtype, {z, dresidual_out, dresidual}) && whole_vectors(W, dout->dtype, {dout, dx});
