@@ -524,14 +524,15 @@ int mss_beam_reorder(const mss_tensor_t* const* states, int count, const mss_ten
  *   x             (..., W)   f32 or bf16, 2 to 4 dimensions
  *   residual      (..., W)   f32 or bf16, nullable
  *   weight        (W,)       f32
- *   eps           not negative
+ *   eps           not negative (MSS_ERR_SHAPE otherwise, and for a NaN)
  *   out           (..., W)   dtype of x, or MSS_F8E4M3 with scales, written
  *   residual_out  (..., W)   dtype of residual, written; given with residual alone; may be residual (in place)
  *   rstd          (...)      f32, nullable, written: for the backward
  *   scales        (..., 1) or (..., ceil(W / 128))   f32, written; given with an 8-bit out alone
  * W is at most 16384 (MSS_ERR_UNSUPPORTED above).  No other overlap of an output.  Sums are fp32: a row with
- * |z| above 1e18 may overflow its sum of squares, and then gives 0.  A NaN, or an infinity, in a row makes its outputs
- * NaN, or 0 beside the infinity.
+ * |z| above 1e18 may overflow its sum of squares, and then gives 0; with an eps of 0 a row of zeros gives NaN, and one whose
+ * squares all underflow (|z| under 1e-23) infinities.  A NaN, or an infinity, in a row makes its outputs NaN, or 0 beside the
+ * infinity.
  */
 int mss_rms_norm_fwd(const mss_tensor_t* x, const mss_tensor_t* residual, const mss_tensor_t* weight, float eps,
                      const mss_tensor_t* out, const mss_tensor_t* residual_out, const mss_tensor_t* rstd,

@@ -62,7 +62,7 @@ int mss_rms_norm_fwd(const mss_tensor_t* x, const mss_tensor_t* residual, const 
         if (!scales && out->dtype == MSS_F8E4M3) return MSS_ERR_NULL_ARG;
         if (x->ndim < 2) return MSS_ERR_SHAPE;
         const int64_t W = x->shape[x->ndim - 1], parts = (W + 127) / 128;
-        if (W < 1 || !shape_is(*weight, 1, W)) return MSS_ERR_SHAPE;
+        if (W < 1 || !shape_is(*weight, 1, W) || !(eps >= 0.0f)) return MSS_ERR_SHAPE;
         for (const mss_tensor_t* t : {residual, out, residual_out})
             if (t && !same_shape(t, *x)) return MSS_ERR_SHAPE;
         if (!lead_is(rstd, *x) || (!lead_is(scales, *x, 1) && !lead_is(scales, *x, parts))) return MSS_ERR_SHAPE;
