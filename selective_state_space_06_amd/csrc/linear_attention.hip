@@ -754,39 +754,50 @@ __global__ __launch_bounds__(256) void attention_update_kernel(AttnUpdateLaunch 
 // segments (at most 128) fill the CUs better but need the states between them: a pass over keys and values at 0.6 (eight
 // waves) or 0.3 (four) of the walk, and a launch; and then to be added up, a microsecond a part of 128 x 128 state in the
 // blocks that read them, or in a launch more.  The pass, whose blocks wait for nothing, is cut further, into parts of 128
-// steps or more, up to a block for every CU.
-// Times by the number of segments, the one that is taken in brackets: 4 x 2048 x 32 heads of 128 x 128 bf16, 1 to 4: 121,
-// [104], 113, 120 us; 4 x 2048 x 80 of 128 x 64 bf16: 127, 125, [117], 128; 3 x 1531 x 12 of 64 x 96 f32, 4, 6, 8, 16: 55,
-// [51], 66, 53; 1 x 2048 x 32 of 128 x 128 bf16, keys and values of 8 heads, 4, 6, 8, 16: 65, 60, 55, [56].
+// steps or more, up to a block for every CU; the parts are what is added up (priced by segments, 1 x 1000 x 4 heads of
+// 64 x 64 f32 28 us instead of 21).
+// Times by the number of segments, the one that is taken in brackets: 4 x 2048 x 32 heads of 128 x 128 bf16, 1 to 4: 139,
+// [108], 118, 117 us; 4 x 2048 x 80 of 128 x 64 bf16, queries and keys of 8 heads: 155, 143, [135], 146; 3 x 1531 x 12 of
+// 64 x 96 f32, 4, 5, 6, 8, 24: 55, 49, [47], 67, 65; 1 x 2048 x 32 of 128 x 128 bf16, keys and values of 8 heads, 4, 6, 8, 16:
+// 65, 59, [52], 55.
 struct Plan {
     int nseg, nparts, cuts;
     int64_t part_steps, cost;
 };
-// Blocks that find room on a CU by registers and LDS: 16 waves, eight in fp32, four of them with more than 64 keys.
-int blocks_a_cu(bool bf16, int waves, int Kd) { return std::max(1, (bf16 ? 16 : Kd > 64 ? 4 : 8) / waves); }
+// Blocks that find room on a CU by registers and LDS: 16 waves; in fp32 three blocks of four waves with up to 64 keys, one of any
+// other kind.  (Three and not two: gradients of 2 x 4096 x 16 heads of 64 x 64 184 -> 176 us, 6 x 1531 x 50 heads forward 152 ->
+// 156.)
+int blocks_a_cu(bool bf16, int waves, int Kd) { return bf16 ? 16 / waves : waves == 4 && Kd <= 64 ? 3 : 1; }
+// Parts of each segment but the last: as many as give a block for every CU, of 128 steps or more.
+int cuts_of(int64_t heads, int64_t segs, int64_t segment) {
+    int cuts = 1;
+    while (segs > 1 && segment % (2 * cuts) == 0 && segment / (2 * cuts) >= 2 && heads * (segs - 1) * cuts < 256) cuts *= 2;
+    return cuts;
+}
 // blocks: of each segment; heads: whose states are wanted; waves: of a block, of one of those that make states
 Plan plan_segments(bool bf16, int Kd, int Vd, int64_t blocks, int64_t heads, int waves, int state_waves, int64_t L) {
     const int64_t steps64 = std::max<int64_t>(1, (L + 63) / 64), most = blocks_a_cu(bf16, waves, Kd);
     const auto time_of = [&](int64_t c) {
         return waves == 16 ? 13 * c : std::max<int64_t>(c > 0 ? 10 : 0, waves == 8 ? 9 * c : 1 + 7 * c);
     };
-    int64_t best = 0, segment = steps64;
+    int64_t best = 0, segment = 0, each = 0;
     for (int64_t n = 1; n <= std::min<int64_t>(128, steps64); ++n) {
-        const int64_t each = (steps64 + n - 1) / n, segs = (steps64 + each - 1) / each;  // of 64 steps, and how many there are
+        if ((steps64 + n - 1) / n == each) continue;
+        each = (steps64 + n - 1) / n;
+        const int64_t segs = (steps64 + each - 1) / each;  // of 64 steps, and how many there are
         const int64_t c = (blocks * segs + 255) / 256;
         int64_t cost = (c / most * time_of(most) + (c % most ? time_of(c % most) : 0)) * (each + 1);
         if (segs > 1) {
+            const int64_t parts = (segs - 1) * cuts_of(heads, segs, each);
             cost += (state_waves == 8 ? 6 : 3) * heads * (segs - 1) * each / 256 + 15;
-            cost += segs - 1 <= kFold ? 3 * (segs - 1) * Kd * Vd / (128 * 128) : 15;
+            cost += parts <= kFold ? 3 * parts * Kd * Vd / (128 * 128) : 13;
         }
         if (n == 1 || cost < best) best = cost, segment = each;
     }
     Plan p;
     p.cost = best;
     p.nseg = static_cast<int>((steps64 + segment - 1) / segment);
-    p.cuts = 1;
-    while (p.nseg > 1 && segment % (2 * p.cuts) == 0 && segment / (2 * p.cuts) >= 2 && heads * (p.nseg - 1) * p.cuts < 256)
-        p.cuts *= 2;
+    p.cuts = cuts_of(heads, p.nseg, segment);
     p.part_steps = segment * 64 / p.cuts;
     p.nparts = (p.nseg - 1) * p.cuts;
     return p;
