@@ -575,8 +575,9 @@ int mss_rms_norm_bwd(const mss_tensor_t* z, const mss_tensor_t* weight, const ms
  * 16-byte aligned (MSS_ERR_LAYOUT).  No output may overlap an input or another output.
  * Computed in chunks of 32 steps on the matrix cores; the state is fp32.  bf16 inputs are taken as they are,
  * states, scores and what enters the state to 2^-25; f32 inputs, whose size is below 3.38e38, in three bf16
- * parts, products to 2^-24.  An infinity or a NaN in a chunk may reach all its outputs, those before it among them, and
- * all later ones.
+ * parts, products to 2^-24; of values under 2^-100 in size fewer bits count (parts under 2^-126 are taken for 0).  A decay
+ * over n steps is e^(-rate n) to a few 2^-24 of itself, however little is left.  An infinity or a NaN in a chunk may reach
+ * all its outputs, those before it among them, and all later ones.
  */
 int mss_linear_attention_scratch(int64_t batch, int64_t L, int64_t heads, int64_t q_heads, int64_t k_heads,
                                  int64_t v_heads, int64_t key_dim, int64_t value_dim, int64_t* fwd_floats,

@@ -18,8 +18,8 @@
 // next product's operand as it stands, when the other operand's rows are taken in the same order, and what has to be
 // turned is read from LDS by the instruction that turns.
 //
-// What bounds it: neither memory nor the matrix cores, but the instructions of a chunk and their waits, 2.4 us for 32 steps
-// with 128 x 128 state (272 VALU instructions a wave, 45 of them MFMA, 75 SALU, 37 LDS), of which decaying the state, cutting
+// What bounds it: neither memory nor the matrix cores, but the instructions of a chunk and their waits, 2.7 us for 32 steps
+// with 128 x 128 state (343 VALU instructions a wave, 55 of them MFMA, 79 SALU, 40 LDS), of which decaying the state, cutting
 // it into parts and reading keys turned are most.  So what counts is instructions, and blocks on a CU at once: chunks of 64
 // steps have twice the scores' work and fewer fit, chunks of 16 leave half of the matrix instruction empty.  A long sequence
 // with few heads is cut into segments; the states between them come from a pass over keys and values alone, whose parts are
@@ -36,9 +36,10 @@
 // fp32 inputs are three parts everywhere, with the six products down to 2^-24 (2.7 times the rate of the fp32 matrix
 // instruction).
 //
-// Measured: 4 x 2048 x 32 heads of 128 x 128 bf16 97 us (2.9 TB/s, 178 TFLOP/s of the formula's products), of them states 23;
-// 1 x 32768 x 16 heads of 64 x 64 f32, keys and values of 4, 156 us, of them states 49 and their sums 8; output and gradients of
-// 4 x 2048 x 80 heads of 128 x 64 bf16 with queries and keys of 8 heads 548 us, of 3 x 1531 x 12 heads of 64 x 96 f32 167.
+// Measured, on several cards: 4 x 2048 x 32 heads of 128 x 128 bf16 107 to 112 us (2.5 TB/s, 157 TFLOP/s of the formula's
+// products), of them states 24; 1 x 32768 x 16 heads of 64 x 64 f32, keys and values of 4, 160 to 166 us, of them states 48 and
+// their sums 9; output and gradients of 4 x 2048 x 80 heads of 128 x 64 bf16 with queries and keys of 8 heads 602 us, of
+// 3 x 1531 x 12 heads of 64 x 96 f32 170 to 180.
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -826,8 +827,8 @@ Plan plan_walks(const Sizes& z) {
     return plan_segments(z.bf16, z.Kd, z.Vd, z.Bt * z.outs * z.count, z.Bt * z.H * z.count, z.waves(), columns(z.Vd) / 16, z.L);
 }
 // Batches of a first launch: all, or as many as fill the CUs in whole rounds, when the others, cut finer, are done sooner in
-// one of their own than as the rest of a round (320 blocks of 16 waves: 182 + 64 us and
-// 29 for the states, 327 in one launch).
+// one of their own than as the rest of a round (320 blocks of 16 waves, twice in the gradients
+// of 4 x 2048 x 80 heads of 128 x 64 bf16, queries and keys of 8: 468 us, 535 in one launch each).
 int64_t first_batches(const Sizes& z) {
     const int64_t blocks = z.outs * z.count, room = 256 * blocks_a_cu(z.bf16, z.waves(), z.Kd);
     const int64_t first = z.Bt * blocks / room * room / blocks;

@@ -5,10 +5,11 @@
 // r = 1 / sqrt(mean z^2 + eps), y = z r w.  Backward, with zh = z r: dz = r (w dy - zh mean(w dy zh)) + dstream,
 // dw = sum over rows of dy zh.  Both are bound by memory: each tensor is read or written once.  A block holds a row in
 // registers (its waves on successive tiles of 512 columns, eight to a lane) between the sum and the outputs.  Forward, a
-// block per row: 8192 x 4096 bf16 47.8 us (5.6 TB/s), into 8 bits with a scale per row 44.9 (5.2 TB/s), 8192 x 2560 bf16 with
-// the stream in fp32 48.5 (5.2 TB/s); blocks that keep their weights and go over rows in turn 50.0, 50.3 and 51.4, and no
-// better with the next row on its way.  Backward, a block goes over rows in turn and keeps its sums of dw, in 64 bits and
-// rounded once; a second kernel joins them in a fixed order, in 64 bits too: 6123 x 2049 f32, forward and backward, 84 us (4.8 TB/s).
+// block per row: 8192 x 4096 bf16 47.8 us (5.6 TB/s), 8192 x 2560 bf16 with the stream in fp32 48.1 (5.2 TB/s), 4096 x 5120
+// into 8 bits with a scale per row 29.2 (5.0 TB/s); blocks that keep their weights and go over rows in turn 4 to 8% slower,
+// and no better with the next row on its way.  Backward, a block goes over rows in turn and keeps its sums of dw, in 64 bits
+// and rounded once; a second kernel joins them in a fixed order, in 64 bits too: 6123 x 2049 f32, forward and backward, 83 us
+// (5.4 TB/s).
 #include <algorithm>
 
 #include "device_math.hpp"
@@ -308,7 +309,7 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* part, int64_t
 
 // Waves a block and tiles a wave for rows of W columns.  One tile a wave as long as 16 waves reach: 8192 x 8192 bf16 92 us, 97
 // with two.  But blocks that wait twice, for the row's greatest value too, are better small enough for several on a CU: into 8
-// bits with a scale per row 8192 x 8192 114 us with one tile, 83 with two, 4096 x 5120 37.8 and 31.3 (8192 x 2560 44.1 and 46.4).
+// bits with a scale per row 8192 x 8192 117 us with one tile, 83 with two, 4096 x 5120 35.0 and 27.8 (8192 x 4096 43.0 and 39.1).
 struct NormPlan {
     int waves, nt;
 };
@@ -318,8 +319,8 @@ NormPlan plan_norm(int64_t W, bool f8) {
     return {(tiles + nt - 1) / nt, nt};
 }
 // The backward's blocks: ten waves for every CU, each block with the same number of rows, at least four if the CUs have work
-// then, since a block's sums of dw are written and read again.  6123 x 2049 f32 47 us, 8192 x 2560 bf16 with z in f32 68, 2048 x
-// 1024 f32 11.7; 16 waves a CU and rows as they come 52, 80 and 20.9 (but 8192 x 5120 bf16 72 and 68).
+// then, since a block's sums of dw are written and read again.  6123 x 2049 f32 45.6 us, 8192 x 2560 bf16 with z in f32 67.3, 2048
+// x 1024 f32 13.8; 16 waves a CU and rows as they come 44.2, 69.1 and 16.7 (8192 x 5120 bf16 72.4 and 72.7).
 int64_t bwd_blocks(int64_t R, int64_t W) {
     if (R == 0) return 0;
     const int64_t most = 256 * std::max(1, 10 / plan_norm(W, false).waves);

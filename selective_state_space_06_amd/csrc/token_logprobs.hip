@@ -14,7 +14,7 @@
 // weigh it (it comes to 1.5 times the entropy in units of 2^-24 at most), and in gradients that are rounded to bf16.  An f32
 // gradient of an improbable token is such a term alone, and has it corrected (exact_exp; the time is the same).
 //
-// Both are bound by memory where there is enough of it: 4096 x 50280 bf16 80 us forward (5.2 TB/s), 230 with the gradient
+// Both are bound by memory where there is enough of it: 4096 x 50280 bf16 80 to 88 us forward (4.7 to 5.2 TB/s), 230 with the gradient
 // (5.4 TB/s).  A batch of 128 x 128007 bf16 takes 14 us without alternatives (2.4 TB/s; 6.4 at the rate of a copy, the rest is
 // the ends of two launches), 19 with 5 of them and 23 with 20; as lists kept by every wave along its way 14, 23 and 39.  One row
 // of 50277 f32 with 20 alternatives takes 14 us, mostly latencies in a row: launches, loads, merges.
