@@ -309,7 +309,8 @@ __global__ __launch_bounds__(1024) void rms_dw_kernel(const float* part, int64_t
 
 // Waves a block and tiles a wave for rows of W columns.  One tile a wave as long as 16 waves reach: 8192 x 8192 bf16 92 us, 97
 // with two.  But blocks that wait twice, for the row's greatest value too, are better small enough for several on a CU: into 8
-// bits with a scale per row 8192 x 8192 117 us with one tile, 83 with two, 4096 x 5120 35.0 and 27.8 (8192 x 4096 43.0 and 39.1).
+// bits with a scale per row 8192 x 8192 117 us with one tile, 83 with two, 4096 x 5120 37.5 and 31.1.  Up to 4096 columns the wait
+// costs as much as two tiles' fewer waves: 8192 x 2560 with the stream in fp32 44.5 and 46.8, in bf16 32.6 and 29.9.
 struct NormPlan {
     int waves, nt;
 };
